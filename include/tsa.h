@@ -74,7 +74,8 @@ typedef enum tsa_status {
   TSA_ERR_DEVICE_BOUNDS = 6  /* a device-side index check failed              */
 } tsa_status;
 
-typedef enum tsa_dtype { TSA_F32 = 0, TSA_BF16 = 1 } tsa_dtype;
+/* TSA_I8 and TSA_E4M3 are types of a paged cache only. */
+typedef enum tsa_dtype { TSA_F32 = 0, TSA_BF16 = 1, TSA_I8 = 2, TSA_E4M3 = 3 } tsa_dtype;
 
 /* Problem shape.  scale <= 0 selects 1/sqrt(D), the 1/sqrt(head dim) of
  * [P1] Step 1 and Step 3. */
@@ -326,6 +327,112 @@ TSA_API tsa_status tsa_drift(int64_t rows, int32_t hidden, int32_t dtype, const 
  */
 TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t window, double threshold,
                                     int32_t* stable);
+
+/*
+ * Paged key/value cache of one layer: what comes before and after the sparse
+ * prefill of the calls above.  New tokens' keys and values are written into
+ * pages (tsa_cache_write), in the layer's type or in 8 bits; new tokens attend
+ * over everything that is cached (tsa_attend_paged: a chunk of a prompt, single
+ * tokens of a decoding step, or a mix); a cached prefix is read back in the
+ * layout that tsa_score and tsa_attend take (tsa_cache_read).
+ *
+ * Pools   k_pages, v_pages [n_pages][Hkv][page_size][D] in cache_dtype: the
+ *         layer's dtype, TSA_I8 or TSA_E4M3.  8-bit pools have one float scale
+ *         for each row of D values: k_scales, v_scales [n_pages][Hkv][page_size];
+ *         a row stands for the values code * scale.  NULL scales otherwise.
+ * Table   page_table int32 [n_seqs][max_pages]: position j of sequence s is slot
+ *         j % page_size of page page_table[s][j / page_size].  Entries beyond
+ *         the sequence's length are not read.  Pages may be shared by sequences.
+ * Lengths seq_len int32 [n_seqs]: cached tokens of each sequence, the new ones of
+ *         this call among them.  token_start int32 [n_seqs + 1], ascending: the
+ *         new tokens of sequence s are the packed rows token_start[s] to
+ *         token_start[s + 1] - 1, at its positions seq_len[s] - n to
+ *         seq_len[s] - 1; n may be 0.
+ *         Table and lengths are DEVICE memory, read by the kernels: a captured
+ *         call follows them.
+ * Rows    packed activations tsa_rows: element [token][head][d] at
+ *         data + token * token_stride + head * head_stride + d, strides in
+ *         elements, non-negative, multiples of 16 bytes; n_tokens rows in all,
+ *         heads Hq (q, out) or Hkv (k, v).  [tokens][heads][D] and
+ *         [heads][tokens][D] are both of this form.  Written rows must not
+ *         overlap one another.  Rows that belong to no sequence (behind the last
+ *         one, say, where a batch is padded) are neither read nor written.
+ *
+ * Supported: D 64 or 128; G = Hq / Hkv in {1, 2, 4, 8, 16}; dtype TSA_F32 or
+ * TSA_BF16; page_size a power of two from 16 to 1024; n_seqs <= 1024;
+ * n_tokens * Hq < 2^31; n_pages * Hkv * page_size < 2^31;
+ * max_pages * page_size < 2^31.  max_new is the largest number of new tokens of
+ * a sequence: it chooses the kernels and the workspace's size; results do not
+ * depend on it.  scale <= 0 selects 1/sqrt(D).
+ *
+ * `ws` is a device workspace of tsa_paged_workspace_size() bytes with the rules
+ * of the calls above (zero-filled once; one stream at a time, captured graphs
+ * included).  TSA_ERR_INVALID_ARG for a NULL or misaligned (16 bytes; table and
+ * lengths 4) pointer, a bad size or stride, or scales that do not go with
+ * cache_dtype; TSA_ERR_UNSUPPORTED outside the shapes; TSA_ERR_WORKSPACE.
+ * TSA_ERR_DEVICE_BOUNDS (status word): token_start outside the packed rows or
+ * descending, a length below its new tokens or beyond max_pages * page_size, a
+ * needed page outside the pool.  Nothing outside the buffers is read or written
+ * then; the rows of the sequences concerned are unspecified.
+ */
+typedef struct tsa_paged_desc {
+  int32_t n_tokens, n_seqs, Hq, Hkv, D;
+  int32_t dtype, cache_dtype; /* tsa_dtype */
+  int32_t page_size, n_pages, max_pages, max_new;
+  float scale;
+} tsa_paged_desc;
+
+typedef struct tsa_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* token_start;
+} tsa_paged_cache;
+
+typedef struct tsa_rows {
+  void* data;
+  int64_t token_stride, head_stride;
+} tsa_rows;
+
+/* Bytes of device workspace of the three calls below; 0 for an invalid shape. */
+TSA_API size_t tsa_paged_workspace_size(const tsa_paged_desc* desc);
+
+/*
+ * tsa_cache_write -- the new tokens' keys and values into their pages.  8-bit
+ * pools, for each row x of D values with a = max |x| and M = 127 (TSA_I8) or 448
+ * (TSA_E4M3): scale = a / M in float, code = the quotient x M / a rounded to the
+ * nearest code, ties to even (the exact quotient decides).  A row of zeros gets
+ * scale 0, a row with a NaN or an infinity codes 0 and scale NaN (it reads back
+ * as NaN).  No two of the call's tokens may share a slot.  One kernel launch.
+ */
+TSA_API tsa_status tsa_cache_write(const tsa_paged_desc* desc, const tsa_paged_cache* cache, const tsa_rows* k,
+                                   const tsa_rows* v, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * tsa_cache_read -- the reverse: packed row t of k and v receives the cached row
+ * of the position that t has (token_start, seq_len as above; a whole sequence is
+ * read with token_start[s + 1] - token_start[s] = seq_len[s]).  8-bit codes give
+ * code * scale in float, rounded to dtype.  One kernel launch.
+ */
+TSA_API tsa_status tsa_cache_read(const tsa_paged_desc* desc, const tsa_paged_cache* cache, const tsa_rows* k,
+                                  const tsa_rows* v, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * tsa_attend_paged -- causal attention of the new tokens over the cache, in which
+ * their own keys and values have been written:
+ *   out[t, h] = sum_{j <= p} softmax_j(scale * q[t, h] . k_j) v_j,
+ * p the position of t in its sequence, k_j and v_j the cached rows of KV head
+ * h / G.  Sums, maxima and accumulators are in float; the result is rounded once
+ * to dtype.  bf16: probabilities, and 8-bit rows of chunks, are rounded to bf16
+ * before the second product.  Cached rows that a token does not see do not
+ * influence its result, whatever they hold.  The work is split along the cached
+ * tokens too and joined in a fixed order: equal calls give equal bits.
+ */
+TSA_API tsa_status tsa_attend_paged(const tsa_paged_desc* desc, const tsa_paged_cache* cache, const tsa_rows* q,
+                                    const tsa_rows* out, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, return the device status recorded in `ws` (TSA_OK,
  * TSA_ERR_TIMEOUT or TSA_ERR_DEVICE_BOUNDS) and clear it.  ws = NULL reads

@@ -15,7 +15,7 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtsa.so")
 
-TSA_F32, TSA_BF16 = 0, 1
+TSA_F32, TSA_BF16, TSA_I8, TSA_E4M3 = 0, 1, 2, 3
 STATUS_NAMES = {0: "TSA_OK", 1: "TSA_ERR_INVALID_ARG", 2: "TSA_ERR_UNSUPPORTED", 3: "TSA_ERR_WORKSPACE",
                 4: "TSA_ERR_CUDA", 5: "TSA_ERR_TIMEOUT", 6: "TSA_ERR_DEVICE_BOUNDS"}
 STATUS = {v: k for k, v in STATUS_NAMES.items()}
@@ -25,12 +25,27 @@ EXPORTED = ("tsa_workspace_size", "tsa_workspace_init", "tsa_score", "tsa_select
             "tsa_debug_wait_never_set", "tsa_debug_launch_count", "tsa_debug_cta_pair_launch_count", "tsa_score_noalloc",
             "tsa_attend_accumulate", "tsa_drift_workspace_size", "tsa_drift", "tsa_layer_stable",
             "tsa_select_coverage", "tsa_forward_coverage", "tsa_attend_block_sparse", "tsa_debug_exp2", "tsa_zero_dropped",
-            "tsa_out_proj_workspace_size", "tsa_out_proj", "tsa_forward_host_h2d_bytes")
+            "tsa_out_proj_workspace_size", "tsa_out_proj", "tsa_forward_host_h2d_bytes",
+            "tsa_paged_workspace_size", "tsa_cache_write", "tsa_cache_read", "tsa_attend_paged")
 
 
 class TsaDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("L", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class TsaPagedDesc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("n_tokens", "n_seqs", "Hq", "Hkv", "D", "dtype", "cache_dtype", "page_size",
+                                              "n_pages", "max_pages", "max_new")] + [("scale", ctypes.c_float)]
+
+
+class TsaPagedCache(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k_pages", "v_pages", "k_scales", "v_scales", "page_table", "seq_len",
+                                               "token_start")]
+
+
+class TsaRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class TsaError(RuntimeError):
@@ -73,7 +88,11 @@ _SIGS = {
     "tsa_drift": (ctypes.c_int, [ctypes.c_int64, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
     "tsa_layer_stable": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), _I32, _I32, ctypes.c_double,
                                         ctypes.POINTER(ctypes.c_int32)]),
+    "tsa_paged_workspace_size": (_SZ, [ctypes.POINTER(TsaPagedDesc)]),
 }
+for _name in ("tsa_cache_write", "tsa_cache_read", "tsa_attend_paged"):
+    _SIGS[_name] = (ctypes.c_int, [ctypes.POINTER(TsaPagedDesc), ctypes.POINTER(TsaPagedCache), ctypes.POINTER(TsaRows),
+                                   ctypes.POINTER(TsaRows), _P, _SZ, _P])
 
 
 def lib() -> ctypes.CDLL:
@@ -311,3 +330,113 @@ def tsa_attend_block_sparse(desc, q, k, v, perm, budgets, block_mask, out, ws, s
 def tsa_debug_exp2(x, y, stream=None):
     """y = 2^x through the library's FMA-pipe exponential (testing hook)."""
     _check(lib().tsa_debug_exp2(_ptr(x), _ptr(y), x.numel(), _stream(stream)), "tsa_debug_exp2")
+
+
+_DTYPES = {torch.float32: TSA_F32, torch.bfloat16: TSA_BF16, torch.int8: TSA_I8, torch.float8_e4m3fn: TSA_E4M3}
+
+
+def make_paged_desc(n_tokens: int, n_seqs: int, Hq: int, Hkv: int, D: int, dtype, cache_dtype, page_size: int, n_pages: int,
+                    max_pages: int, max_new: int, scale: float = 0.0) -> TsaPagedDesc:
+    """Shape of the paged-cache calls (include/tsa.h); dtype float32 or bfloat16, cache_dtype the same,
+    ``torch.int8`` or ``torch.float8_e4m3fn``."""
+    return TsaPagedDesc(n_tokens, n_seqs, Hq, Hkv, D, _DTYPES.get(dtype, -1), _DTYPES.get(cache_dtype, -1), page_size, n_pages,
+                        max_pages, max_new, float(scale))
+
+
+class PagedCache:
+    """The buffers of one layer's paged cache: pools ``k_pages`` / ``v_pages`` [n_pages, Hkv, page_size, D], int32
+    ``page_table`` [n_seqs, max_pages], ``seq_len`` [n_seqs] and ``token_start`` [n_seqs + 1], and for 8-bit pools
+    float32 ``k_scales`` / ``v_scales`` [n_pages, Hkv, page_size].  All contiguous and on one device.  The buffers
+    are referenced, not copied: lengths and table entries are changed in place between calls."""
+
+    __slots__ = ("_tensors", "_c", "_shape", "device")
+
+    def __init__(self, k_pages, v_pages, page_table, seq_len, token_start, k_scales=None, v_scales=None):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, D] of one type")
+        if k_pages.dtype not in _DTYPES:
+            raise ValueError("pages must be float32, bfloat16, int8 or float8_e4m3fn")
+        quantised = _DTYPES[k_pages.dtype] in (TSA_I8, TSA_E4M3)
+        if quantised != (k_scales is not None) or quantised != (v_scales is not None):
+            raise ValueError("8-bit pages need k_scales and v_scales, other pages have none")
+        scales = (k_scales, v_scales) if quantised else ()
+        for t in scales:
+            if t.dtype != torch.float32 or t.shape != k_pages.shape[:3]:
+                raise ValueError("scales must be float32 [n_pages, Hkv, page_size]")
+        ints = (page_table, seq_len, token_start)
+        if any(t.dtype != torch.int32 for t in ints):
+            raise ValueError("page_table, seq_len and token_start must be int32")
+        if page_table.dim() != 2 or seq_len.shape != page_table.shape[:1] or tuple(token_start.shape) != (seq_len.shape[0] + 1,):
+            raise ValueError("page_table must be [n_seqs, max_pages], seq_len [n_seqs], token_start [n_seqs + 1]")
+        self._tensors = (k_pages, v_pages, k_scales, v_scales, page_table, seq_len, token_start)
+        self.device = k_pages.device
+        for t in self._tensors:
+            if t is not None and (not t.is_contiguous() or t.device != self.device):
+                raise ValueError("the cache's tensors must be contiguous and on one device")
+        self._c = TsaPagedCache(*[_ptr(t) for t in self._tensors])
+        n_pages, Hkv, page_size, D = k_pages.shape
+        self._shape = (n_pages, Hkv, page_size, D, _DTYPES[k_pages.dtype], page_table.shape[0], page_table.shape[1])
+
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    k_scales = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+    page_table = property(lambda self: self._tensors[4])
+    seq_len = property(lambda self: self._tensors[5])
+    token_start = property(lambda self: self._tensors[6])
+
+
+def tsa_paged_workspace_size(desc: TsaPagedDesc) -> int:
+    return int(lib().tsa_paged_workspace_size(ctypes.byref(desc)))
+
+
+def alloc_paged_workspace(desc: TsaPagedDesc, device="cuda") -> torch.Tensor:
+    """Workspace of the three paged-cache calls, zero-filled."""
+    n = tsa_paged_workspace_size(desc)
+    if n == 0:
+        raise TsaError(STATUS["TSA_ERR_INVALID_ARG"], "tsa_paged_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _rows(t: torch.Tensor, desc: TsaPagedDesc, heads: int, device) -> TsaRows:
+    if t.shape != (desc.n_tokens, heads, desc.D) or _DTYPES.get(t.dtype) != desc.dtype or t.stride(2) != 1:
+        raise ValueError(f"expected packed rows [{desc.n_tokens}, {heads}, {desc.D}] of the layer's type with unit last stride")
+    if t.device != device:
+        raise ValueError(f"tensor on {t.device}, cache on {device}")
+    return TsaRows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _paged_call(name: str, desc, cache, a, b, heads: int, ws, stream):
+    if cache._shape != (desc.n_pages, desc.Hkv, desc.page_size, desc.D, desc.cache_dtype, desc.n_seqs, desc.max_pages):
+        raise ValueError(f"{name}: the cache's buffers do not have the shape that desc says")
+    device = cache.device
+    ra, rb = _rows(a, desc, heads, device), _rows(b, desc, heads, device)
+    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"{name}: the workspace must be contiguous uint8 on the cache's device")
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    stream = getattr(stream, "cuda_stream", stream)
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        code = f(desc, cache._c, ra, rb, ws.data_ptr(), ws.numel(), stream)
+    else:
+        with torch.cuda.device(device):
+            code = f(desc, cache._c, ra, rb, ws.data_ptr(), ws.numel(), stream)
+    _check(code, name)
+
+
+def tsa_cache_write(desc, cache, k, v, ws, stream=None):
+    """The new tokens' keys and values [n_tokens, Hkv, D] into their pages (8-bit pools: codes and scales)."""
+    _paged_call("tsa_cache_write", desc, cache, k, v, desc.Hkv, ws, stream)
+
+
+def tsa_cache_read(desc, cache, k, v, ws, stream=None):
+    """k and v [n_tokens, Hkv, D] receive the cached rows at their tokens' positions."""
+    _paged_call("tsa_cache_read", desc, cache, k, v, desc.Hkv, ws, stream)
+
+
+def tsa_attend_paged(desc, cache, q, out, ws, stream=None):
+    """out [n_tokens, Hq, D]: causal attention of the new tokens q over everything cached up to their own positions."""
+    _paged_call("tsa_attend_paged", desc, cache, q, out, desc.Hq, ws, stream)

@@ -1,0 +1,101 @@
+// 8-bit codes of the paged cache: rounding on the way in, exact conversions on
+// the way out.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace tsa {
+
+// Code kinds of a cache as template arguments.
+constexpr int kPlain = 0, kI8 = 1, kE4M3 = 2;
+
+template <int CODE>
+__device__ __forceinline__ constexpr float code_max() {
+  return CODE == kI8 ? 127.f : 448.f;
+}
+
+// |x| M / a for a row whose largest magnitude is a > 0, rounded so that rounding
+// it once more to the code's grid gives what the exact quotient would.
+//
+// The quotient is the product with 1 / a and one correction by its remainder
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): a quotient that fp32 holds, so every tie of a grid of at
+// most 8 bits, comes out exact.  With 8-bit significands (bf16 rows) no other
+// quotient lies within 2^-16 of a border between two codes, so this decides
+// every case.  fp32 rows can come closer: next to a border b the sign of
+// x M - b a decides.  Both products are known exactly there: x M as its rounded
+// value and the remainder of the rounding, and x M - b a because b has at most
+// 8 bits and the two agree in at least 12.
+// x, a: scaled by the row's power of two so that no product over- or underflows.
+template <int CODE, bool WIDE>
+__device__ __forceinline__ float code_quotient(float x, float a, float r) {
+  constexpr float M = code_max<CODE>();
+  const float p = x * M;
+  const float t0 = p * r;
+  float t = fmaf(fmaf(-t0, a, p), r, t0);
+  if (WIDE) {
+    float b;
+    bool close;
+    if (CODE == kI8) {
+      b = floorf(t) + 0.5f;
+      close = fabsf(t - b) < 1e-4f;
+    } else if (t < 0.015625f) {  // below 2^-6 the grid is 2^-9
+      b = (floorf(t * 512.f) + 0.5f) * 0.001953125f;
+      close = fabsf(t - b) < 1e-7f;
+    } else {
+      const uint32_t u = __float_as_uint(t);
+      b = __uint_as_float((u & 0xFFF00000u) | 0x00080000u);
+      close = (u & 0xFFFFFu) - 0x7FFF0u <= 0x20u;
+    }
+    if (close) {
+      const float s = fmaf(-b, a, p) + fmaf(x, M, -p);
+      const uint32_t ub = __float_as_uint(b);
+      t = s > 0.f ? __uint_as_float(ub + 1) : s < 0.f ? __uint_as_float(ub - 1) : b;
+    }
+  }
+  return t;
+}
+
+// Two bytes of `w` (at bits 0-7 and 16-23; the rest is ignored) as int8 -> bf16x2.
+// With the low seven bits in the mantissa of 128 .. 255, code + 128 (or + 256
+// where the sign is set) is a bf16 number, and the difference is exact.
+__device__ __forceinline__ uint32_t i8_pair(uint32_t w) {
+  const uint32_t a = (w & 0x007f007fu) | 0x43004300u;  // 128 + low bits
+  const uint32_t b = (w & 0x00800080u) | 0x43004300u;  // 128, or 256 for a negative code
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two bytes at bits 8-15 and 24-31 as e4m3 -> bf16x2: the fields shifted into
+// place give the value times 2^-120 (bias 127 against 7), subnormals included.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
+  const uint32_t r = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(r), "r"(0x7B807B80u));  // 2^120
+  return y;
+}
+
+// bf16x2 of the codes in bytes i and i + 1 of w (i = 0 or 2).
+template <int CODE, int I>
+__device__ __forceinline__ uint32_t codes_next(uint32_t w) {
+  if (CODE == kI8) return i8_pair(__byte_perm(w, 0, I == 0 ? 0x4140 : 0x4342));
+  return e4m3_pair(__byte_perm(w, 0, I == 0 ? 0x1404 : 0x3424));
+}
+// bf16x2 of byte B of w0 and byte B of w1.
+template <int CODE, int B>
+__device__ __forceinline__ uint32_t codes_across(uint32_t w0, uint32_t w1) {
+  constexpr uint32_t sel = (uint32_t)B | ((uint32_t)B << 4) | ((uint32_t)(B + 4) << 8) | ((uint32_t)(B + 4) << 12);
+  const uint32_t w = __byte_perm(w0, w1, sel);
+  return CODE == kI8 ? i8_pair(w) : e4m3_pair(w);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+}  // namespace tsa

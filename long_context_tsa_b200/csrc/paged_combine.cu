@@ -1,0 +1,79 @@
+// Joins the partial tiles of the paged attention kernels.
+//
+// Part i of a tile has the reference m_i, the sum l_i and the unnormalised o_i;
+// with m = max m_i the result is sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,
+// added in the order of the CTAs that left the parts.  A few MB that the kernel
+// before has just written: read from L2, bound by latency.
+#include <math.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "paged.h"
+#include "paged_codes.cuh"
+
+namespace tsa {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = 8;  // rows of a block
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts parts) {
+  const PartMeta meta = parts.meta[blockIdx.x];
+  if (meta.c_end < 0) return;
+  const int first = blockIdx.x, n = min(meta.c_end, parts.ctas - 1) - first + 1;
+  const int rp_log2 = 7 - p.g_log2;
+  for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+    // Neighbouring threads take neighbouring float4s of the parts' layout.
+    const int lr = parts.by_head ? i % kRows : i / (D / 4);
+    const int c4 = parts.by_head ? i / kRows : i % (D / 4);
+    const int row = blockIdx.y * kRows + lr;
+    int tok, head;
+    if (parts.by_head) {
+      tok = ((row >> 7) << rp_log2) + (row & ((1 << rp_log2) - 1));
+      head = (row & 127) >> rp_log2;
+    } else {
+      tok = row >> p.g_log2;
+      head = row & (p.G - 1);
+    }
+    if (tok >= meta.n_tok) continue;
+    auto slot = [&](int k) { return (size_t)(first + k) * 2 + (k == 0 ? 1 : 0); };
+    float top = -INFINITY;
+    for (int k = 0; k < n; ++k) top = fmaxf(top, parts.ml[slot(k) * 2 * parts.rows + row]);
+    float sum = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < n; ++k) {
+      const float m = parts.ml[slot(k) * 2 * parts.rows + row];
+      const float f = m == top ? 1.f : exp2f(m - top);
+      sum += f * parts.ml[(slot(k) * 2 + 1) * parts.rows + row];
+      const float4 o = *reinterpret_cast<const float4*>(parts.o + slot(k) * parts.rows * D + row * parts.row_stride + c4 * parts.c4_stride);
+      a.x += f * o.x;
+      a.y += f * o.y;
+      a.z += f * o.z;
+      a.w += f * o.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw no key: zeros
+    T* dst = static_cast<T*>(out.data) + (int64_t)(meta.tok0 + tok) * out.ts + (int64_t)(meta.g * p.G + head) * out.hs + c4 * 4;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st) {
+  const dim3 grid(parts.ctas, (parts.rows + kRows - 1) / kRows);
+  if (p.dtype == TSA_BF16) {
+    if (p.D == 64) paged_combine<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(p, out, parts);
+    else paged_combine<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(p, out, parts);
+  } else {
+    if (p.D == 64) paged_combine<float, 64><<<grid, kThreads, 0, st>>>(p, out, parts);
+    else paged_combine<float, 128><<<grid, kThreads, 0, st>>>(p, out, parts);
+  }
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace tsa
