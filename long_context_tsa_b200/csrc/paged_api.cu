@@ -93,7 +93,12 @@ tsa_status check_rows(const tsa_rows* r, const Paged& p, int heads, bool written
   return TSA_OK;
 }
 
-size_t workspace_bytes(const Paged& p) { return kHeaderBytes + paged_simt_bytes(p); }
+// bf16 queries: short sequences go to the kernel for few rows.
+bool use_small(const Paged& p) { return p.dtype == TSA_BF16 && (long long)p.max_new * p.G <= kSplitRows; }
+
+size_t workspace_bytes(const Paged& p) {
+  return kHeaderBytes + (use_small(p) ? paged_small_bytes(p) : paged_simt_bytes(p));
+}
 
 // The checks that the three calls share; a and b: the packed tensors.
 tsa_status check_call(const tsa_paged_desc* desc, const tsa_paged_cache* cache, const tsa_rows* a, const tsa_rows* b,
@@ -148,7 +153,9 @@ tsa_status tsa_attend_paged(const tsa_paged_desc* desc, const tsa_paged_cache* c
   Rows rq, ro;
   const tsa_status s = check_call(desc, cache, q, out, true, false, true, ws, ws_bytes, &p, &rq, &ro);
   if (s != TSA_OK) return s;
-  return cuda_status(launch_paged_simt(p, rq, ro, static_cast<char*>(ws) + kHeaderBytes, static_cast<cudaStream_t>(stream)));
+  void* parts = static_cast<char*>(ws) + kHeaderBytes;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(use_small(p) ? launch_paged_small(p, rq, ro, parts, 0, st) : launch_paged_simt(p, rq, ro, parts, st));
 }
 
 }  // extern "C"

@@ -1,0 +1,658 @@
+// Attention of a few new tokens over the paged cache (bf16 queries): single
+// tokens of a decoding step, and short runs of up to 32 rows, a row being a new
+// token and one of the G query heads of the KV head.
+//
+// Bound by reading the cache: per cached token and KV head 4 D bytes (bf16) or
+// 2 D + 8 (8-bit) against 4 G D flops a new token.  So the tile is one of 16 or
+// 32 rows in registers (mma.sync m16n8k16: with so few rows the tensor rate is no
+// concern, and accumulators in registers need no round trip through TMEM), and
+// everything else serves to keep loads in flight:
+//
+// - The run of key tiles of a CTA (paged_plan.cuh) is cut over its 8 warps, 16
+//   keys of each 128 to a warp.  Warps share nothing until a tile of rows ends:
+//   each has its own ring of TMA boxes (16 keys never cross a page), its own
+//   running reference and sum, its own accumulators.  A warp's ring runs across
+//   the ends of tiles, so loads never pause for the join of a tile.
+// - 8-bit codes become bf16 without rounding (both kinds are exact in bf16); the
+//   scale of a key multiplies its logits, the scale of a value its probability,
+//   both in fp32.  Codes are read as whole 16-byte pieces of a row: the order of
+//   the contraction index d, of the 16 keys and of the output columns is free as
+//   long as both operands agree, and is chosen so that a thread's pieces are
+//   contiguous and a quarter warp's fall into different banks.
+// - The reference m of the softmax moves only when a logit passes it by 2^8
+//   (P <= 2^8, bf16's relative precision is the same there), found with one vote
+//   a block; the sum over a row's four threads waits until the tile ends.
+//
+// P is rounded to bf16 for the second product (relative 2^-9, the precision of
+// the output); sums, references and accumulators are fp32.
+//
+// A masked key has P = 0 exactly, also where its scale is not finite.  A value
+// row that is not finite and hidden from some row of the tile would still give
+// 0 * inf: where the causal border crosses the 16 keys, non-finite values of an
+// unscaled cache are added to the rows that see them and cleared in the tile.
+#include <cuda.h>
+#include <math.h>
+
+#include "internal.h"
+#include "paged.h"
+#include "paged_codes.cuh"
+#include "paged_plan.cuh"
+#include "tc_ptx.cuh"
+#include "tma_maps.h"
+
+namespace tsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kKeys = 16;               // keys of a warp in a unit of 128
+constexpr float kMoveReference = 8.f;   // log2 units
+constexpr uint32_t kDrainPolls = 1u << 26;
+
+template <int D, int CODE, int MT>
+struct Cfg {
+  static constexpr int ESZ = CODE == kPlain ? 2 : 1;
+  static constexpr int KV_BYTES = kKeys * D * ESZ;       // K or V of 16 keys
+  static constexpr int STAGE = 2 * KV_BYTES;
+  static constexpr int RING = (CODE == kPlain ? 192 : 160) * 1024 / kWarps;  // bytes of a warp's ring: what the join leaves
+  static constexpr int NS = RING / STAGE > 8 ? 8 : RING / STAGE;
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int OFF_RING = 0;
+  static constexpr int OFF_JOIN = kWarps * NS * STAGE;   // 4 partial tiles of 16 rows
+  static constexpr int OFF_SCALE = OFF_JOIN + 4 * 16 * D * 4;
+  static constexpr int SCALE_BYTES = CODE == kPlain ? 0 : kWarps * NS * 2 * kKeys * 4;
+  static constexpr int OFF_ML = OFF_SCALE + SCALE_BYTES;  // [8 warps][ROWS][m, l]
+  static constexpr int OFF_BAR = OFF_ML + kWarps * ROWS * 8;
+  static constexpr int OFF_PLAN = OFF_BAR + kWarps * NS * 8;
+  static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanSmem);
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static constexpr int NKS = D / 16;  // k steps of QK
+  static constexpr int NNT = D / 8;   // column tiles of O
+};
+
+struct SmallParams {
+  Paged p;
+  Rows q, out;
+  Parts parts;
+  Plan plan;
+  float scale_log2;
+  uint64_t wait_limit;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Untiled bulk copy global -> shared; both addresses and the size multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// The order of keys, contraction index and output columns inside a block of 16 keys.
+template <int D, int CODE>
+struct Order {
+  // Key of index n (0..7) of a column tile of S, and of index k = 2j, 2j+1 of P.
+  __device__ static __forceinline__ int key(int n) {
+    return CODE != kPlain && D == 128 ? (n >> 1) | ((n & 1) << 2) : n;
+  }
+  // Piece of an 8-bit V row that thread row c (0..7) reads.
+  __device__ static __forceinline__ int piece(int c) { return D == 128 ? (c >> 1) | ((c & 1) << 2) : c; }
+  // First column d of output index n (0..7): column tile nt is at first + nt (8-bit) or 8 nt + n.
+  __device__ static __forceinline__ int col(int n, int nt) {
+    return CODE == kPlain ? 8 * nt + n : piece(n) * (D / 8) + nt;
+  }
+};
+
+template <int D, int CODE, int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_small(const __grid_constant__ SmallParams P, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D, CODE, MT>;
+  using O = Order<D, CODE>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const Paged& p = P.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rg = lane >> 2, qj = lane & 3;  // fragment row and column group
+  PlanSmem* psm = reinterpret_cast<PlanSmem*>(smem + C::OFF_PLAN);
+  float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+  const uint32_t ring = sbase + C::OFF_RING + warp * C::NS * C::STAGE;
+  const uint32_t sscale = sbase + C::OFF_SCALE + warp * C::NS * (2 * kKeys * 4);
+  const uint32_t bar = sbase + C::OFF_BAR + warp * C::NS * 8;
+
+  if (lane == 0) {
+    for (int s = 0; s < C::NS; ++s) mbar_init(bar + 8 * s, 1);
+    fence_mbar_init();
+  }
+  Cursor cur;
+  long long left, run;
+  plan_start<kThreads>(p, P.plan, psm, &cur, &left, &run);
+  if (threadIdx.x == 0) P.parts.meta[blockIdx.x].c_end = -1;
+  if (left == 0) return;
+
+  // ---- loads: a cursor of their own, up to NS blocks ahead of the products.
+  Cursor lc = cur;
+  long long l_left = left;
+  int l_keys = P.plan.keys(lc.span, lc.j), l_units = P.plan.units(lc.span, lc.j);
+  uint32_t issued = 0, l_stage = 0;  // blocks loaded so far
+  int l_entry = 0;                   // page table entry of the next block, read one block ahead
+  auto l_lookup = [&]() {
+    const int key0 = (lc.kt << 7) + warp * kKeys;
+    if (l_left > 0 && key0 < l_keys) l_entry = __ldg(p.table + (size_t)lc.s * p.max_pages + (key0 >> p.page_log2));
+  };
+  l_lookup();
+  // Steps over units without keys of this warp; loads one block if there is one.
+  auto load_next = [&]() {
+    while (l_left > 0) {
+      const int key0 = (lc.kt << 7) + warp * kKeys;
+      const bool has = key0 < l_keys;
+      if (has) {
+        const int page = checked_page(p, l_entry);
+        const size_t row = (((size_t)page * p.Hkv + lc.g) << p.page_log2) + (key0 & ((1 << p.page_log2) - 1));
+        const uint32_t dst = ring + l_stage * C::STAGE, b = bar + 8 * l_stage;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b, C::STAGE + (CODE == kPlain ? 0 : 2 * kKeys * 4));
+          if constexpr (CODE == kPlain) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * 2048, &kmap, b, h * 64, (int)row);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + C::KV_BYTES + h * 2048, &vmap, b, h * 64, (int)row);
+          } else {  // rows of 128 bytes: one key (D = 128) or two (D = 64)
+            const int y = (int)(D == 128 ? row : row >> 1);
+            tma_load_2d(dst, &kmap, b, 0, y);
+            tma_load_2d(dst + C::KV_BYTES, &vmap, b, 0, y);
+            bulk_load(sscale + l_stage * 128, p.k_scales + row, 64, b);
+            bulk_load(sscale + l_stage * 128 + 64, p.v_scales + row, 64, b);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        l_stage = l_stage + 1 == C::NS ? 0 : l_stage + 1;
+      }
+      --l_left;
+      if (++lc.kt >= l_units && l_left > 0) {
+        plan_next(p, P.plan, &lc);
+        l_keys = P.plan.keys(lc.span, lc.j);
+        l_units = P.plan.units(lc.span, lc.j);
+      }
+      l_lookup();
+      if (has) return;
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::NS; ++i) load_next();
+
+  uint32_t used = 0, stage = 0, phase = 0;
+  bool ok = true;
+  const int tt = 1 << P.plan.tt_log2;
+
+  while (left > 0) {
+    // ------------------------------------------------ one tile of rows, or a part of it
+    const int keys = P.plan.keys(cur.span, cur.j), units = P.plan.units(cur.span, cur.j);
+    const int kt1 = (int)min((long long)units, cur.kt + left);
+    const int first_tok = cur.j * tt;
+    const int n_tok = min(tt, cur.span.n - first_tok);
+    const int pos0 = cur.span.base + first_tok;  // position of the tile's first token
+    const int n_rows = n_tok << p.g_log2;
+
+    // Queries as A fragments: thread (rg, qj) holds rows rg, rg + 8 at the d of its k indices.
+    uint32_t qa[MT][C::NKS][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = min(mt * 16 + rg + 8 * hf, n_rows - 1);
+        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(P.q.data) +
+                                  (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
+                                  (int64_t)(cur.g * p.G + (r & (p.G - 1))) * P.q.hs;
+        if constexpr (CODE == kPlain) {
+#pragma unroll
+          for (int ks = 0; ks < C::NKS; ++ks) {
+            qa[mt][ks][hf] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * qj));
+            qa[mt][ks][hf + 2] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * qj));
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)  // 16 codes of a piece: four k steps of four
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(qr + 64 * h + 16 * qj + 8 * x));
+              qa[mt][4 * h + 2 * x][hf] = v.x;
+              qa[mt][4 * h + 2 * x][hf + 2] = v.y;
+              qa[mt][4 * h + 2 * x + 1][hf] = v.z;
+              qa[mt][4 * h + 2 * x + 1][hf + 2] = v.w;
+            }
+        }
+      }
+    int rpos[MT][2];  // position of the thread's rows: they see keys up to it
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) rpos[mt][hf] = pos0 + min((mt * 16 + rg + 8 * hf) >> p.g_log2, n_tok - 1);
+
+    float m[MT][2], l[MT][2], o[MT][C::NNT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < C::NNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+    }
+
+#pragma unroll 1
+    for (int kt = cur.kt; kt < kt1; ++kt) {
+      const int key0 = (kt << 7) + warp * kKeys;
+      if (key0 >= keys) break;  // later units have none either
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * stage, phase, P.wait_limit, nullptr));
+      if (!ok) break;
+      const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::KV_BYTES;
+      // Rows hide keys behind their own position; keys from `keys` on are not of this sequence.
+      const bool border = key0 + kKeys - 1 > pos0;
+
+      if (CODE == kPlain && border) {
+        // Values that some row must not see: clear what lies behind the tile's last key, and
+        // take non-finite values out of the product (they reach the rows that see them here).
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < kKeys * D * 2 / 512; ++i) {
+          const int at = i * 32 + lane;            // 16-byte piece: row, piece
+          const int row = at / (D / 8), pc = at % (D / 8);
+          const uint32_t addr = sv + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
+          if (key0 + row >= keys) {
+            st_shared_v4(addr, 0u, 0u, 0u, 0u);
+          } else if (key0 + row > pos0) {
+            const uint4 x = lds128(addr);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= ((((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0);
+          }
+        }
+        __syncwarp();
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+          for (int row = 0; row < kKeys; ++row) {
+            if (key0 + row <= pos0 || key0 + row >= keys) continue;
+#pragma unroll
+            for (int nt = 0; nt < C::NNT; ++nt) {  // the two columns 8 nt + 2 qj of this thread's accumulators
+              const uint32_t addr = sv + (nt >> 3) * 2048 + row * 128 + (((nt & 7) ^ (row & 7)) << 4) + 4 * qj;
+              const uint32_t w = __float_as_uint(lds32(addr));
+              const float x0 = bf16_lo(w), x1 = bf16_hi(w);
+              const bool b0 = !(fabsf(x0) < INFINITY), b1 = !(fabsf(x1) < INFINITY);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                  if (b0 && key0 + row <= rpos[mt][hf]) o[mt][nt][2 * hf] += x0;
+                  if (b1 && key0 + row <= rpos[mt][hf]) o[mt][nt][2 * hf + 1] += x1;
+                }
+              __syncwarp();
+              if (rg == 0 && (b0 || b1))
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"((b0 ? 0u : w & 0xffffu) | (b1 ? 0u : w & 0xffff0000u)) : "memory");
+            }
+          }
+        }
+        fence_proxy_async_smem();  // the ring's next TMA box overwrites these stores
+        __syncwarp();
+      }
+
+      // ---- S = Q K^T over 16 keys: two column tiles of 8
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+      if constexpr (CODE == kPlain) {
+        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < C::NKS; ++ks) {
+          const int pc = 2 * ks + half;
+          uint32_t b[4];
+          ldsm4(b, sk + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(s[mt][0], qa[mt][ks], b[0], b[1]);
+            mma16816(s[mt][1], qa[mt][ks], b[2], b[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = 8 * n + O::key(rg);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            uint32_t addr;
+            if (D == 128) addr = sk + key * 128 + (((4 * h + qj) ^ (key & 7)) << 4);
+            else addr = sk + (key >> 1) * 128 + ((((key & 1) * 4 + qj) ^ ((key >> 1) & 7)) << 4);
+            const uint4 v = lds128(addr);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t b0 = codes_next<CODE, 0>(w[x]), b1 = codes_next<CODE, 2>(w[x]);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][n], qa[mt][4 * h + x], b0, b1);
+            }
+          }
+        }
+      }
+
+      // ---- softmax: columns 2 qj, 2 qj + 1 of each column tile
+      float vs[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int key = 8 * n + O::key(2 * qj + e);
+          float f = P.scale_log2;
+          if constexpr (CODE != kPlain) {
+            f *= lds32(sscale + stage * 128 + 4 * key);
+            vs[n][e] = lds32(sscale + stage * 128 + 64 + 4 * key);
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            s[mt][n][e] *= f;
+            s[mt][n][e + 2] *= f;
+            if (border) {
+              if (key0 + key > rpos[mt][0] || key0 + key >= keys) s[mt][n][e] = -INFINITY;
+              if (key0 + key > rpos[mt][1] || key0 + key >= keys) s[mt][n][e + 2] = -INFINITY;
+            }
+          }
+        }
+      bool move = false;
+      float mx[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          mx[mt][hf] = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]), fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+          move |= mx[mt][hf] > m[mt][hf] + kMoveReference;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float x = mx[mt][hf];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            if (x > m[mt][hf] + kMoveReference) {
+              // Before the first key o holds zeros, or infinities that the border's values have just added.
+              const float alpha = m[mt][hf] == -INFINITY ? 1.f : ex2_approx(m[mt][hf] - x);
+              m[mt][hf] = x;
+              l[mt][hf] *= alpha;
+#pragma unroll
+              for (int nt = 0; nt < C::NNT; ++nt) {
+                o[mt][nt][2 * hf] *= alpha;
+                o[mt][nt][2 * hf + 1] *= alpha;
+              }
+            }
+          }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];  // no key seen yet: 2^-inf = 0
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float p0 = ex2_approx(s[mt][n][2 * hf] - ref), p1 = ex2_approx(s[mt][n][2 * hf + 1] - ref);
+            l[mt][hf] += p0 + p1;
+            if constexpr (CODE != kPlain) {
+              p0 *= vs[n][0];
+              p1 *= vs[n][1];
+              if (border) {  // the scale of a key that is not seen may be anything
+                if (s[mt][n][2 * hf] == -INFINITY) p0 = 0.f;
+                if (s[mt][n][2 * hf + 1] == -INFINITY) p1 = 0.f;
+              }
+            }
+            pa[mt][2 * n + hf] = pack_bf16x2(p0, p1);
+          }
+        }
+
+      // ---- O += P V
+      if constexpr (CODE == kPlain) {
+        const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int pc = 2 * i + (lane >> 4);
+          uint32_t b[4];
+          ldsm4_t(b, sv + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(o[mt][2 * i], pa[mt], b[0], b[1]);
+            mma16816(o[mt][2 * i + 1], pa[mt], b[2], b[3]);
+          }
+        }
+      } else {
+        uint32_t w[4][D / 32];  // the thread's four keys, D / 8 columns each
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int key = 8 * (x >> 1) + O::key(2 * qj + (x & 1));
+          if constexpr (D == 128) {
+            const uint4 v = lds128(sv + key * 128 + ((O::piece(rg) ^ (key & 7)) << 4));
+            w[x][0] = v.x;
+            w[x][1] = v.y;
+            w[x][2] = v.z;
+            w[x][3] = v.w;
+          } else {
+            const uint2 v = lds64(sv + (key >> 1) * 128 + ((((key & 1) * 4 + (rg >> 1)) ^ ((key >> 1) & 7)) << 4) + (rg & 1) * 8);
+            w[x][0] = v.x;
+            w[x][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t b[4][2] = {
+              {codes_across<CODE, 0>(w[0][i], w[1][i]), codes_across<CODE, 0>(w[2][i], w[3][i])},
+              {codes_across<CODE, 1>(w[0][i], w[1][i]), codes_across<CODE, 1>(w[2][i], w[3][i])},
+              {codes_across<CODE, 2>(w[0][i], w[1][i]), codes_across<CODE, 2>(w[2][i], w[3][i])},
+              {codes_across<CODE, 3>(w[0][i], w[1][i]), codes_across<CODE, 3>(w[2][i], w[3][i])}};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * i + x], pa[mt], b[x][0], b[x][1]);
+        }
+      }
+      __syncwarp();  // every lane has read the stage before it is filled again
+      ++used;
+      if (++stage == C::NS) {
+        stage = 0;
+        phase ^= 1;
+      }
+      load_next();
+    }
+
+    // ------------------------------------------------ join the warps' parts
+    const int did = kt1 - cur.kt;
+    const bool whole = cur.kt == 0 && kt1 == units;
+    const int slot = cur.kt == 0 ? 1 : 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
+        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+        if (qj == 0) ml[warp * C::ROWS + mt * 16 + rg + 8 * hf] = make_float2(m[mt][hf], l[mt][hf]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float f[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::ROWS + mt * 16 + rg + 8 * hf].x);
+        f[hf] = m[mt][hf] == top ? 1.f : ex2_approx(m[mt][hf] - top);
+      }
+      float* mine = join + (warp & 3) * 16 * D;
+      auto at = [&](int hf, int nt, int e) -> float& {  // column groups of 8 swapped by row against bank conflicts
+        const int r = rg + 8 * hf, d = O::col(2 * qj + e, nt);
+        return mine[r * D + (d ^ ((r & 3) << 3))];
+      };
+      if (warp >= 4) {
+#pragma unroll
+        for (int nt = 0; nt < C::NNT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) = o[mt][nt][e] * f[e >> 1];
+      }
+      __syncthreads();
+      if (warp < 4) {
+#pragma unroll
+        for (int nt = 0; nt < C::NNT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) += o[mt][nt][e] * f[e >> 1];
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * D / 4; i += kThreads) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        const int row = mt * 16 + r;
+        if (row >= n_rows) continue;
+        const int dd = d ^ ((r & 3) << 3);
+        float4 a = *reinterpret_cast<const float4*>(join + r * D + dd);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+          const float4 b = *reinterpret_cast<const float4*>(join + w * 16 * D + r * D + dd);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::ROWS + row].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 x = ml[w * C::ROWS + row];
+          sum += (x.x == top ? 1.f : ex2_approx(x.x - top)) * x.y;
+        }
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw no key: zeros
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(P.out.data) +
+                               (int64_t)(cur.span.tok0 + first_tok + (row >> p.g_log2)) * P.out.ts +
+                               (int64_t)(cur.g * p.G + (row & (p.G - 1))) * P.out.hs + d;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        } else {
+          const size_t part = (size_t)blockIdx.x * 2 + slot;
+          *reinterpret_cast<float4*>(P.parts.o + (part * C::ROWS + row) * D + d) = a;
+          if (d == 0) {
+            P.parts.ml[(part * 2) * C::ROWS + row] = top;
+            P.parts.ml[(part * 2 + 1) * C::ROWS + row] = sum;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x == 0 && cur.kt == 0 && kt1 < units) {
+      PartMeta mt;
+      mt.c_end = plan_last_cta(p, units - kt1, run);
+      mt.g = cur.g;
+      mt.tok0 = cur.span.tok0 + first_tok;
+      mt.n_tok = n_tok;
+      P.parts.meta[blockIdx.x] = mt;
+    }
+    left -= did;
+    if (left > 0) plan_next(p, P.plan, &cur);
+  }
+
+  if (!ok && lane == 0) {  // a wait ran out: no copy may still be writing when the CTA exits
+    record_status(p.status, TSA_ERR_TIMEOUT);
+    for (; used != issued; ++used) {
+      mbar_wait(bar + 8 * stage, phase, kDrainPolls, nullptr);
+      if (++stage == C::NS) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+template <int D, int CODE, int MT>
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
+  using C = Cfg<D, CODE, MT>;
+  SmallParams P;
+  P.p = p;
+  P.q = q;
+  P.out = out;
+  P.parts = make_parts(base, C::ROWS, kPagedCtas, D);
+  P.plan.which = which;
+  P.plan.kt_log2 = 7;
+  P.plan.tt_log2 = (MT == 2 ? 5 : 4) - p.g_log2;
+  P.scale_log2 = p.scale * 1.4426950408889634f;
+  P.wait_limit = wait_limit();
+  const uint64_t rows = ((uint64_t)p.n_pages * p.Hkv) << p.page_log2;
+  CUtensorMap km, vm;
+  const bool made = CODE == kPlain ? make_tile_map(&km, p.k_pages, rows, D, kKeys) && make_tile_map(&vm, p.v_pages, rows, D, kKeys)
+                                   : make_code_map(&km, p.k_pages, rows * D / 128, kKeys * D / 128) &&
+                                         make_code_map(&vm, p.v_pages, rows * D / 128, kKeys * D / 128);
+  if (!made) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(paged_small<D, CODE, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  paged_small<D, CODE, MT><<<kPagedCtas, kThreads, C::SMEM, st>>>(P, km, vm);
+  count_launches(1);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_paged_combine(p, out, P.parts, st);
+}
+
+// Up to 16 rows (a row tile of one mma) the second row tile would be empty.
+bool one_tile(const Paged& p) { return (long long)p.max_new * p.G <= 16; }
+
+template <int D, int CODE>
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
+  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, which, st) : launch<D, CODE, 2>(p, q, out, base, which, st);
+}
+
+template <int D>
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
+  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, which, st);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, which, st);
+  return by_rows<D, kPlain>(p, q, out, base, which, st);
+}
+
+}  // namespace
+
+size_t paged_small_bytes(const Paged& p) { return parts_bytes(one_tile(p) ? 16 : 32, kPagedCtas, p.D); }
+
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* parts_base, int which, cudaStream_t st) {
+  return p.D == 64 ? by_code<64>(p, q, out, parts_base, which, st) : by_code<128>(p, q, out, parts_base, which, st);
+}
+
+}  // namespace tsa

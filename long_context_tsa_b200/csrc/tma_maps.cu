@@ -23,14 +23,15 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
-bool encode(CUtensorMap* m, const void* base, uint64_t rows, int D, uint32_t box_rows) {
+bool encode(CUtensorMap* m, const void* base, uint64_t rows, int D, uint32_t box_rows,
+            CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int elem = 2) {
   EncodeTiled enc = encode_fn();
   if (enc == nullptr) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D * elem};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -41,6 +42,10 @@ bool make_row_map(CUtensorMap* m, const void* base, uint64_t rows, int D) { retu
 
 bool make_tile_map(CUtensorMap* m, const void* base, uint64_t rows, int D, int box_rows) {
   return encode(m, base, rows, D, (uint32_t)box_rows);
+}
+
+bool make_code_map(CUtensorMap* m, const void* base, uint64_t rows, int box_rows) {
+  return encode(m, base, rows, 128, (uint32_t)box_rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1);
 }
 
 }  // namespace tsa

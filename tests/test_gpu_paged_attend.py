@@ -91,6 +91,34 @@ def test_hidden_rows_may_hold_anything(dtype, cache, n):
     assert torch.isnan(out[n - 1]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,at", [(3, 0), (6, 2), (8, 7), (100, 0), (140, 131), (300, 257)])
+def test_an_infinite_value_among_the_first_keys(dtype, n, at):
+    c = Layer([(n, n)], Hkv=1, G=4, D=64, dtype=dtype, page=16, seed=n)
+    q = c.packed(4)
+    want = attend(c, q)
+    c.v_pages[int(c.table[0, at // 16]), 0, at % 16, 9] = -float("inf")
+    got = attend(c, q)
+    want[at:, :, 9] = -float("inf")
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("cache", [None, "int8"])
+@pytest.mark.parametrize("n", [1, 100])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(cache, n):
+    c = Layer([(3000, n)] * 3, Hkv=2, G=4, D=128, cache=cache, page=64)
+    q = c.packed(8)
+    out = c.packed(8, random=False)
+    T.tsa_debug_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            T.tsa_attend_paged(c.desc, c.cache, q, out, c.ws)
+            assert T.tsa_check_status(c.ws) in (0, 5)  # a single poll may also find the copy landed
+    finally:
+        T.tsa_debug_set_wait_limit(0)
+    c.check(attend(c, q), q)
+
+
 @pytest.mark.parametrize("dtype,cache", CACHES)
 def test_length_below_new_tokens_gives_zeros_to_rows_without_keys(dtype, cache):
     c = Layer([(60, 40), (33, 1)], Hkv=2, G=2, D=64, dtype=dtype, cache=cache, page=16)
