@@ -74,6 +74,8 @@ cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, vo
 // which: 0 every sequence, 1 those with at most kSplitRows rows, 2 the others.
 size_t paged_small_bytes(const Paged& p);
 cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* parts_base, int which, cudaStream_t st);
+size_t paged_chunk_bytes(const Paged& p);
+cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* parts_base, int which, cudaStream_t st);
 // Joins the partial tiles that a kernel left behind.
 cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st);
 

@@ -93,11 +93,24 @@ tsa_status check_rows(const tsa_rows* r, const Paged& p, int heads, bool written
   return TSA_OK;
 }
 
-// bf16 queries: short sequences go to the kernel for few rows.
-bool use_small(const Paged& p) { return p.dtype == TSA_BF16 && (long long)p.max_new * p.G <= kSplitRows; }
+tsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSA_OK : TSA_ERR_CUDA; }
+
+// f32 runs on CUDA cores.  bf16: short sequences go to the kernel for few rows,
+// longer ones to the kernel for chunks; a batch that may hold both kinds takes
+// both, each doing its own.
+bool all_short(const Paged& p) { return (long long)p.max_new * p.G <= kSplitRows; }
 
 size_t workspace_bytes(const Paged& p) {
-  return kHeaderBytes + (use_small(p) ? paged_small_bytes(p) : paged_simt_bytes(p));
+  if (p.dtype != TSA_BF16) return kHeaderBytes + paged_simt_bytes(p);
+  return kHeaderBytes + (all_short(p) ? paged_small_bytes(p) : paged_chunk_bytes(p));
+}
+
+cudaError_t launch_attend(const Paged& p, const Rows& q, const Rows& out, void* parts, cudaStream_t st) {
+  if (p.dtype != TSA_BF16) return launch_paged_simt(p, q, out, parts, st);
+  if (all_short(p)) return launch_paged_small(p, q, out, parts, 0, st);
+  if (p.S == 1) return launch_paged_chunk(p, q, out, parts, 0, st);
+  const cudaError_t e = launch_paged_small(p, q, out, parts, 1, st);
+  return e != cudaSuccess ? e : launch_paged_chunk(p, q, out, parts, 2, st);
 }
 
 // The checks that the three calls share; a and b: the packed tensors.
@@ -114,8 +127,6 @@ tsa_status check_call(const tsa_paged_desc* desc, const tsa_paged_cache* cache, 
   p->status = static_cast<uint32_t*>(ws);
   return TSA_OK;
 }
-
-tsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSA_OK : TSA_ERR_CUDA; }
 
 }  // namespace
 }  // namespace tsa
@@ -153,9 +164,7 @@ tsa_status tsa_attend_paged(const tsa_paged_desc* desc, const tsa_paged_cache* c
   Rows rq, ro;
   const tsa_status s = check_call(desc, cache, q, out, true, false, true, ws, ws_bytes, &p, &rq, &ro);
   if (s != TSA_OK) return s;
-  void* parts = static_cast<char*>(ws) + kHeaderBytes;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(use_small(p) ? launch_paged_small(p, rq, ro, parts, 0, st) : launch_paged_simt(p, rq, ro, parts, st));
+  return cuda_status(launch_attend(p, rq, ro, static_cast<char*>(ws) + kHeaderBytes, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,4 +1,4 @@
-// Attention of new tokens over the paged cache on CUDA cores, in fp32.
+// Attention of f32 new tokens over the paged cache on CUDA cores: exact fp32 products.
 //
 // A tile is ROWS rows of one KV head, row = token * G + query head, against key
 // tiles of 64 cached positions; CTAs take equal runs of (tile, key tile) pairs
@@ -44,9 +44,9 @@ struct SimtParams {
 };
 
 // Sixteen bytes of a cached row (plain) or eight codes of it, as floats.
-template <typename T, int CODE>
+template <int CODE>
 struct Piece {
-  static constexpr int N = CODE != kPlain ? 8 : 16 / (int)sizeof(T);
+  static constexpr int N = CODE != kPlain ? 8 : 4;
   float f[N];
   __device__ __forceinline__ void load(const void* pool, size_t elem, float scale) {
     if constexpr (CODE != kPlain) {
@@ -57,22 +57,14 @@ struct Piece {
         f[2 * e] = bf16_lo(h[e]) * scale;
         f[2 * e + 1] = bf16_hi(h[e]) * scale;
       }
-    } else if constexpr (sizeof(T) == 2) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(pool) + elem));
-      const uint32_t h[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[2 * e] = bf16_lo(h[e]);
-        f[2 * e + 1] = bf16_hi(h[e]);
-      }
     } else {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const T*>(pool) + elem));
+      const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(pool) + elem));
       f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
     }
   }
 };
 
-template <typename T, int CODE, int D, int ROWS>
+template <int CODE, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant__ SimtParams P) {
   using C = Cfg<D, ROWS>;
   constexpr int R = ROWS / 16;  // rows of a thread
@@ -118,14 +110,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
       const int r = i / (D / 4), c = i % (D / 4) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < n_rows) {
-        const T* g = static_cast<const T*>(P.q.data) + (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
+        const float* g = static_cast<const float*>(P.q.data) + (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
                      (int64_t)(cur.g * p.G + (r & (p.G - 1))) * P.q.hs + c;
-        if constexpr (sizeof(T) == 4) {
-          x = *reinterpret_cast<const float4*>(g);
-        } else {
-          const uint2 h = *reinterpret_cast<const uint2*>(g);
-          x = make_float4(bf16_lo(h.x), bf16_hi(h.x), bf16_lo(h.y), bf16_hi(h.y));
-        }
+        x = *reinterpret_cast<const float4*>(g);
       }
       *reinterpret_cast<float4*>(Qs + r * C::KS + c) = x;
     }
@@ -146,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
       const int key0 = kt * kKeys;
       const int* rows = rows_of + (kt & 1) * kKeys;
       __syncthreads();  // rows found; K and V of the previous tile are done with
-      using Pc = Piece<T, CODE>;
+      using Pc = Piece<CODE>;
       constexpr int PPR = D / Pc::N;
 #pragma unroll
       for (int i = tid; i < kKeys * PPR; i += kThreads) {
@@ -255,16 +242,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
       if (row >= n_rows) continue;
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw no key: zeros
-        T* dst = static_cast<T*>(P.out.data) + (int64_t)(cur.span.tok0 + first_tok + (row >> p.g_log2)) * P.out.ts +
+        float* dst = static_cast<float*>(P.out.data) + (int64_t)(cur.span.tok0 + first_tok + (row >> p.g_log2)) * P.out.ts +
                  (int64_t)(cur.g * p.G + (row & (p.G - 1))) * P.out.hs;
 #pragma unroll
         for (int j = 0; j < DJ; ++j) {
           const float4 a = o[i][j];
-          if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float4*>(dst + tx * 4 + 64 * j) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-          else
-            *reinterpret_cast<uint2*>(dst + tx * 4 + 64 * j) =
-                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          *reinterpret_cast<float4*>(dst + tx * 4 + 64 * j) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
         }
       } else {
 #pragma unroll
@@ -292,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
 // Few rows take the small tile: fewer of its rows are empty.
 int rows_log2(const Paged& p) { return (long long)p.max_new * p.G <= 16 ? 4 : 6; }
 
-template <typename T, int CODE, int D, int ROWS>
+template <int CODE, int D, int ROWS>
 cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st) {
   using C = Cfg<D, ROWS>;
   SimtParams P;
@@ -304,24 +287,24 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, c
   P.plan.kt_log2 = 6;
   P.plan.which = 0;
   P.scale_log2 = p.scale * 1.4426950408889634f;
-  cudaError_t e = cudaFuncSetAttribute(paged_simt<T, CODE, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(paged_simt<CODE, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  paged_simt<T, CODE, D, ROWS><<<C::CTAS, kThreads, C::SMEM, st>>>(P);
+  paged_simt<CODE, D, ROWS><<<C::CTAS, kThreads, C::SMEM, st>>>(P);
   count_launches(1);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_paged_combine(p, out, P.parts, st);
 }
 
-template <typename T, int CODE, int D>
+template <int CODE, int D>
 cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st) {
-  return rows_log2(p) == 4 ? launch<T, CODE, D, 16>(p, q, out, base, st) : launch<T, CODE, D, 64>(p, q, out, base, st);
+  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, st) : launch<CODE, D, 64>(p, q, out, base, st);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st) {
-  if (p.cache_dtype == TSA_I8) return by_rows<T, kI8, D>(p, q, out, base, st);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<T, kE4M3, D>(p, q, out, base, st);
-  return by_rows<T, kPlain, D>(p, q, out, base, st);
+  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, st);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, st);
+  return by_rows<kPlain, D>(p, q, out, base, st);
 }
 
 }  // namespace
@@ -329,9 +312,7 @@ cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, 
 size_t paged_simt_bytes(const Paged& p) { return parts_bytes(1 << rows_log2(p), 2 * kPagedCtas, p.D); }
 
 cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* parts_base, cudaStream_t st) {
-  if (p.dtype == TSA_BF16)
-    return p.D == 64 ? by_code<__nv_bfloat16, 64>(p, q, out, parts_base, st) : by_code<__nv_bfloat16, 128>(p, q, out, parts_base, st);
-  return p.D == 64 ? by_code<float, 64>(p, q, out, parts_base, st) : by_code<float, 128>(p, q, out, parts_base, st);
+  return p.D == 64 ? by_code<64>(p, q, out, parts_base, st) : by_code<128>(p, q, out, parts_base, st);
 }
 
 }  // namespace tsa
