@@ -426,8 +426,8 @@ TSA_API tsa_status tsa_cache_read(const tsa_paged_desc* desc, const tsa_paged_ca
  *   out[t, h] = sum_{j <= p} softmax_j(scale * q[t, h] . k_j) v_j,
  * p the position of t in its sequence, k_j and v_j the cached rows of KV head
  * h / G.  Sums, maxima and accumulators are in float; the result is rounded once
- * to dtype.  bf16: probabilities, and 8-bit rows of chunks, are rounded to bf16
- * before the second product.  Cached rows that a token does not see do not
+ * to dtype.  bf16: probabilities (8-bit pools: times the value row's scale) are
+ * rounded to bf16 for the second product; codes are exact.  Cached rows that a token does not see do not
  * influence its result, whatever they hold.  The work is split along the cached
  * tokens too and joined in a fixed order: equal calls give equal bits.
  */

@@ -70,14 +70,18 @@ struct Cfg {
   static constexpr int TILE = 128 * D * 2;                      // a bf16 K, V or Q tile
   static constexpr int NS = QUANT ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // K/V ring
   static constexpr int NR = QUANT ? 3 : 0;                      // ring of raw code tiles
-  static constexpr int RAW = 128 * D + 512;                     // codes, then 128 scales
+  static constexpr int RAW = 128 * D + 1024;                    // codes, then (K tiles) the scales of 128 keys and values
+  // Scales of a key tile stay until both M tiles' softmax has used them.  The tile that is converted
+  // when V of key tile j has been released is at most NS - 1 tiles further on.
+  static constexpr int SD = QUANT ? NS / 2 + 1 : 0;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_RAW = OFF_KV + NS * TILE;
-  static constexpr int OFF_ODD = OFF_RAW + NR * RAW;            // [3][D] packed first rows of non-finite values
-  static constexpr int OFF_BAR = OFF_ODD + 3 * D * 4;
-  // q[2], qfree, full[NS], empty[NS], s[2], p[2], o[2], teardown, border[NS] or raw_full[NR], raw_empty[NR]
-  static constexpr int NBAR = 3 + 2 * NS + 6 + 1 + (QUANT ? 2 * NR : NS);
+  static constexpr int OFF_SCALE = OFF_RAW + NR * RAW;          // [SD][2][128] floats
+  static constexpr int OFF_ODD = OFF_SCALE + SD * 1024;         // [3][D] packed first rows of non-finite values
+  static constexpr int OFF_BAR = OFF_ODD + (QUANT ? 0 : 3 * D * 4);
+  // q[2], qfree[2], full[NS], empty[NS], s[2], p[2], o[2], teardown, border[NS] or raw_full[NR], raw_empty[NR]
+  static constexpr int NBAR = 4 + 2 * NS + 6 + 1 + (QUANT ? 2 * NR : NS);
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;           // tmem slot, abort flag, odd[3], done[8]
   static constexpr int OFF_PLAN = (OFF_MISC + 64 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanSmem);
@@ -111,6 +115,37 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
+}
+
+// Orders uses of r after an earlier wait for TMEM loads.
+__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, uint32_t x, uint32_t y) {
+  float f, g;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(a), __uint_as_float(b)), f2_pack(__uint_as_float(x), __uint_as_float(y))), f, g);
+  a = __float_as_uint(f);
+  b = __float_as_uint(g);
+}
+
+// Register split: the softmax warps hold a row of S.  The block is launched with 512 x 128
+// registers; 256 x 184 + 256 x 72 is exactly that, and both sides run this before anything else.
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+static_assert(256 * (kSoftmaxRegs + kOtherRegs) <= kThreads * 128, "registers of the block");
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ bool any_odd(uint32_t w) { return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0; }
@@ -161,17 +196,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sQ = base + C::OFF_Q, sKV = base + C::OFF_KV, sRaw = base + C::OFF_RAW;
   const uint32_t bar0 = base + C::OFF_BAR;
   auto bar_q = [&](int t) { return bar0 + 8u * t; };
-  const uint32_t bar_qfree = bar0 + 8u * 2;
-  auto bar_full = [&](int s) { return bar0 + 8u * (3 + s); };
-  auto bar_empty = [&](int s) { return bar0 + 8u * (3 + C::NS + s); };
-  auto bar_s = [&](int t) { return bar0 + 8u * (3 + 2 * C::NS + t); };
-  auto bar_p = [&](int t) { return bar0 + 8u * (5 + 2 * C::NS + t); };
-  auto bar_o = [&](int t) { return bar0 + 8u * (7 + 2 * C::NS + t); };
-  const uint32_t bar_td = bar0 + 8u * (9 + 2 * C::NS);
+  auto bar_qfree = [&](int t) { return bar0 + 8u * (2 + t); };
+  auto bar_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (4 + C::NS + s); };
+  auto bar_s = [&](int t) { return bar0 + 8u * (4 + 2 * C::NS + t); };
+  auto bar_p = [&](int t) { return bar0 + 8u * (6 + 2 * C::NS + t); };
+  auto bar_o = [&](int t) { return bar0 + 8u * (8 + 2 * C::NS + t); };
+  const uint32_t bar_td = bar0 + 8u * (10 + 2 * C::NS);
   // What the preparing warps wait for: V tiles at the border (by ring stage), or raw tiles.
-  auto bar_border = [&](int s) { return bar0 + 8u * (10 + 2 * C::NS + s); };
-  auto bar_rfull = [&](int s) { return bar0 + 8u * (10 + 2 * C::NS + s); };
-  auto bar_rempty = [&](int s) { return bar0 + 8u * (10 + 2 * C::NS + C::NR + s); };
+  auto bar_border = [&](int s) { return bar0 + 8u * (11 + 2 * C::NS + s); };
+  auto bar_rfull = [&](int s) { return bar0 + 8u * (11 + 2 * C::NS + s); };
+  auto bar_rempty = [&](int s) { return bar0 + 8u * (11 + 2 * C::NS + C::NR + s); };
   uint32_t* odd_cols = reinterpret_cast<uint32_t*>(smem + C::OFF_ODD);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -186,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_s(t), 1);
       mbar_init(bar_p(t), 128);
       mbar_init(bar_o(t), 1);
+      mbar_init(bar_qfree(t), 1);
     }
-    mbar_init(bar_qfree, 1);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(bar_full(s), kPrepWarps);  // one arrival of each preparing warp, or as many of the loading one
       mbar_init(bar_empty(s), 1);
@@ -204,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     P.parts.meta[blockIdx.x].c_end = -1;
   }
-  for (int i = threadIdx.x; i < 3 * D; i += kThreads) odd_cols[i] = kNoneOdd;
+  if (!C::QUANT)
+    for (int i = threadIdx.x; i < 3 * D; i += kThreads) odd_cols[i] = kNoneOdd;
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -230,17 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
+  if (warp >= 8) {
+    regs_dec<kOtherRegs>();
   if (warp >= kPrepWarp0 && warp < kPrepWarp0 + kPrepWarps) {
     // ------------------------------------------------------------ preparation
     const int pw = warp - kPrepWarp0;
     uint32_t kv = 0;   // K/V tiles so far: ring stage kv % NS
-    uint32_t raw = 0;  // raw tiles so far
-    uint32_t seen = 0; // phase of each stage's border barrier
+    uint32_t q1_used = 0;  // Q tiles of M tile 1 so far (M tile 0 has one in every segment)
+    [[maybe_unused]] uint32_t seen = 0;  // phase of each stage's border barrier
     walk([&](const Seg& s, int i) -> bool {
       uint32_t* odd = odd_cols + (i % 3) * D;
       // Clear the next segment's notes once every softmax warp has left the segment that used them
       // last.  The other preparing warps write there only after all have arrived on bar_q below.
-      {
+      if constexpr (!C::QUANT) {
         bool free = i < 2 || lane >= 8 || done[lane] >= i - 1;
         for (uint64_t k = 0; k < P.wait_limit && !free && *abort_flag == 0; ++k) {
           __nanosleep(32);
@@ -256,14 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pw == 0 && lane == 0) odd_flag[(i + 1) % 3] = 0;
         __threadfence_block();
       }
-      if (i > 0) {  // the tensor core has read the previous Q tiles
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_qfree, (i - 1) & 1, P.wait_limit, abort_flag))) {
-          if (lane == 0) fail();
-          return false;
-        }
-      }
       const int my_c = lane % C::CPR, my_r = lane / C::CPR;
       for (int t = 0; t < s.nt; ++t) {
+        if (t == 0 ? i > 0 : q1_used > 0) {  // the tensor core has read the Q tile that was here
+          const uint32_t ph = (t == 0 ? (uint32_t)i : q1_used) - 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_qfree(t), ph & 1, P.wait_limit, abort_flag))) {
+            if (lane == 0) fail();
+            return false;
+          }
+        }
+        q1_used += t;
 #pragma unroll 4
         for (int n = 0; n < 32 / C::RPI; ++n) {
           const int row = 32 * pw + n * C::RPI + my_r;
@@ -317,44 +357,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           kv += 2;
         } else {
 #pragma unroll 1
-          for (int is_v = 0; is_v < 2; ++is_v, ++kv, ++raw) {
-            const uint32_t rs = raw % C::NR, st = kv % C::NS;
-            bool got = mbar_wait(bar_rfull(rs), (raw / C::NR) & 1, P.wait_limit, abort_flag);
+          for (int is_v = 0; is_v < 2; ++is_v, ++kv) {
+            const uint32_t rs = kv % C::NR, st = kv % C::NS;
+            bool got = mbar_wait(bar_rfull(rs), (kv / C::NR) & 1, P.wait_limit, abort_flag);
             if (got && kv >= C::NS) got = mbar_wait(bar_empty(st), ((kv / C::NS) - 1) & 1, P.wait_limit, abort_flag);
             if (!__all_sync(0xffffffffu, got)) {
               if (lane == 0) fail();
               return false;
             }
-            const uint32_t src = sRaw + rs * C::RAW, dst = sKV + st * C::TILE;
-            const float* sc = reinterpret_cast<const float*>(smem + C::OFF_RAW + rs * C::RAW + 128 * D);
-            constexpr int PPR = D / 8;  // 8-byte pieces of a code row: one 16-byte chunk of bf16
-#pragma unroll 4
-            for (int n = 0; n < 32 / C::RPI; ++n) {
-              const int row = 32 * pw + n * C::RPI + my_r;
-              const uint2 x = lds64(src + row * D + my_c * 8);
-              const float f = sc[row];
-              const uint32_t h[4] = {codes_next<CODE, 0>(x.x), codes_next<CODE, 2>(x.x), codes_next<CODE, 0>(x.y), codes_next<CODE, 2>(x.y)};
-              uint32_t w[4];
+            if (!is_v) {  // a thread for each key: its scales
+              const int key = 32 * pw + lane;
+              const float* sc = reinterpret_cast<const float*>(smem + C::OFF_RAW + rs * C::RAW + 128 * D);
+              float* to = reinterpret_cast<float*>(smem + C::OFF_SCALE + (kv >> 1) % C::SD * 1024);
+              to[key] = sc[key] * P.scale_log2;
+              to[128 + key] = sc[128 + key];
+            }
+            const uint32_t src = sRaw + rs * C::RAW + (32 * pw + my_r) * D + my_c * 8;
+            const uint32_t dst = sKV + st * C::TILE + (uint32_t)(my_c >> 3) * 16384u;
+            constexpr int B = 8;  // pieces in flight
+#pragma unroll 1
+            for (int n0 = 0; n0 < 32 / C::RPI; n0 += B) {
+              uint2 x[B];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(bf16_lo(h[e]) * f, bf16_hi(h[e]) * f);
-              static_assert(PPR == C::CPR, "chunks of a row");
-              if (border && is_v) {
-                if (key0 + row >= s.keys) {
-                  w[0] = w[1] = w[2] = w[3] = 0u;
-                } else if (key0 + row > s.pos0 && (any_odd(w[0]) || any_odd(w[1]) || any_odd(w[2]) || any_odd(w[3]))) {
+              for (int n = 0; n < B; ++n) x[n] = lds64(src + (n0 + n) * C::RPI * D);
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const uint32_t h16 = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                    if ((h16 & 0x7f80u) == 0x7f80u) {
-                      note_odd(odd + my_c * 8 + e, h16, (uint32_t)(key0 + row - s.pos0));
-                      w[e >> 1] &= 0xffff0000u >> (16 * (e & 1));
-                    }
-                  }
-                  odd_flag[i % 3] = 1;
-                }
+              for (int n = 0; n < B; ++n) {
+                const uint32_t row = 32 * pw + (n0 + n) * C::RPI + my_r;
+                st_shared_v4(dst + row * 128 + ((((uint32_t)my_c ^ row) & 7u) << 4), codes_next<CODE, 0>(x[n].x),
+                             codes_next<CODE, 2>(x[n].x), codes_next<CODE, 0>(x[n].y), codes_next<CODE, 2>(x[n].y));
               }
-              st_shared_v4(dst + (uint32_t)(my_c >> 3) * 16384u + row * 128 + ((((uint32_t)my_c & 7u) ^ ((uint32_t)row & 7u)) << 4),
-                           w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -402,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!C::QUANT) at_border = (at_border & ~(1u << st)) | ((uint32_t)border << st);
           if (border) borders ^= 1u << st;
           if (lane == 0) {
-            mbar_arrive_expect_tx(b, boxes * box * (C::QUANT ? D + 4 : D * 2));
+            mbar_arrive_expect_tx(b, boxes * box * (C::QUANT ? (is_v ? D : D + 8) : D * 2));
             if (!C::QUANT && !border)
               for (int w = 1; w < kPrepWarps; ++w) mbar_arrive(b);
           }
@@ -412,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t dst = sRaw + st * C::RAW;
               const uint8_t* codes = static_cast<const uint8_t*>(is_v ? p.v_pages : p.k_pages);
               bulk_load(dst + (lane << box_log2) * D, codes + row * D, box * D, b);
-              bulk_load(dst + 128 * D + (lane << box_log2) * 4, (is_v ? p.v_scales : p.k_scales) + row, box * 4, b);
+              if (!is_v) {
+                bulk_load(dst + 128 * D + (lane << box_log2) * 4, p.k_scales + row, box * 4, b);
+                bulk_load(dst + 128 * D + 512 + (lane << box_log2) * 4, p.v_scales + row, box * 4, b);
+              }
             } else {
               const uint32_t dst = sKV + st * C::TILE + (lane << box_log2) * 128;
 #pragma unroll
@@ -434,60 +468,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
+    // One thread for both M tiles: their products follow one another whole.  (Two issuing warps,
+    // one for each tile, share the tensor core instruction by instruction, and both tiles' logits
+    // come late: 811 us against 680 for 8192 tokens.)
     if (lane == 0) {
       constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t IDESC_PV = idesc_bf16(128, D, 0, 1);
+      constexpr uint32_t HI = sdesc_hi_sw128(1024);
+      const uint32_t q_lo = sdesc_lo(sQ, 16), k_lo = sdesc_lo(sKV, 16), v_lo = sdesc_lo(sKV, 16384);
       bool ok = true;
-      uint32_t kv = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-      auto wait_tile = [&](uint32_t i) { return mbar_wait(bar_full(i % C::NS), (i / C::NS) & 1, P.wait_limit, abort_flag); };
-      auto qk = [&](int t, uint32_t i) {
-        const uint32_t kbase = sKV + (i % C::NS) * C::TILE, qbase = sQ + t * C::TILE;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_bf16_ss(tmem + (uint32_t)t * 128u, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024), IDESC_QK, kk > 0);
+      uint32_t st = 0, ph = 0;  // ring stage and phase of the next tile
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};
+      auto wait_tile = [&](uint32_t stage, uint32_t phase) { return mbar_wait(bar_full(stage), phase, P.wait_limit, abort_flag); };
+      auto next_tile = [&]() {
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
         }
       };
-      auto pv = [&](int t, uint32_t i, bool acc) {
-        const uint32_t vbase = sKV + (i % C::NS) * C::TILE;
+      auto qk = [&](int t) {
+        const uint32_t a = q_lo + t * (C::TILE >> 4), b = k_lo + st * (C::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(tmem + C::O_COL0 + t * D, tmem + (uint32_t)t * 128u + kk * 8, sdesc_sw128(vbase + kk * 2048, 16384, 1024), IDESC_PV,
-                      (acc || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+          if (kk == 0) mma_bf16_ss_lo<false>(tmem + t * 128u, a + off, b + off, HI, IDESC_QK);
+          else mma_bf16_ss_lo<true>(tmem + t * 128u, a + off, b + off, HI, IDESC_QK);
+        }
       };
       walk([&](const Seg& s, int) -> bool {
         const int m = s.kt1 - s.c.kt;
-        if (!(ok = wait_tile(kv))) return false;
+        if (!(ok = wait_tile(st, ph))) return false;
         for (int t = 0; t < s.nt; ++t) {
           if (!(ok = mbar_wait(bar_q(t), nq[t]++ & 1, P.wait_limit, abort_flag))) return false;
           fence_proxy_async_smem();  // rows landed by cp.async are read by the tensor core
           tc_fence_after();
-          qk(t, kv);
+          qk(t);
           tc_commit(bar_s(t));
+          if (m == 1) tc_commit(bar_qfree(t));
         }
-        tc_commit(bar_empty(kv % C::NS));
-        if (m == 1) tc_commit(bar_qfree);
+        tc_commit(bar_empty(st));
+        next_tile();
         for (int j = 0; j < m; ++j) {
-          const uint32_t iv = kv + 1, ik = kv + 2;
-          kv += 2;
-          if (!(ok = wait_tile(iv))) return false;
+          if (!(ok = wait_tile(st, ph))) return false;
+          const uint32_t v_st = st;
+          next_tile();  // the next key tile's K
           for (int t = 0; t < s.nt; ++t) {
             if (!(ok = mbar_wait(bar_p(t), np[t]++ & 1, P.wait_limit, abort_flag))) return false;
             tc_fence_after();
-            pv(t, iv, j > 0);
-            if (t + 1 == s.nt) tc_commit(bar_empty(iv % C::NS));
+            const uint32_t a = tmem + t * 128u, d = tmem + C::O_COL0 + t * D, b = v_lo + v_st * (C::TILE >> 4);
+            if (j == 0) mma_bf16_ts_lo<false>(d, a, b, HI, IDESC_PV);
+            else mma_bf16_ts_lo<true>(d, a, b, HI, IDESC_PV);
+#pragma unroll
+            for (int kk = 1; kk < 8; ++kk) mma_bf16_ts_lo<true>(d, a + kk * 8, b + kk * 128, HI, IDESC_PV);
             if (j + 1 < m) {
-              if (t == 0 && !(ok = wait_tile(ik))) return false;
-              tc_fence_after();
-              qk(t, ik);
-              tc_commit(bar_s(t));
-              if (t + 1 == s.nt) {
-                tc_commit(bar_empty(ik % C::NS));
-                if (j + 2 == m) tc_commit(bar_qfree);
+              if (t == 0) {
+                if (!(ok = wait_tile(st, ph))) return false;
+                tc_fence_after();
               }
+              qk(t);
+              tc_commit(bar_s(t));
+              if (j + 2 == m) tc_commit(bar_qfree(t));
             } else {
               tc_commit(bar_o(t));
             }
+          }
+          tc_commit(bar_empty(v_st));
+          if (j + 1 < m) {
+            tc_commit(bar_empty(st));
+            next_tile();
           }
         }
         return true;
@@ -497,8 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(bar_td, 0, kDrainPolls, nullptr);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  }
+  } else {
     // ------------------------------------------------------------ softmax + epilogue
+    regs_inc<kSoftmaxRegs>();
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -506,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + C::O_COL0 + t * D;
     const int hh = r >> P.rp_log2, tok = (t << P.rp_log2) + (r & ((1 << P.rp_log2) - 1));
     uint32_t ns = 0, no = 0;
+    [[maybe_unused]] uint32_t unit = 0;  // key tiles so far
     bool ok = true;
     walk([&](const Seg& s, int i) -> bool {
       auto leave = [&]() {
@@ -515,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (t >= s.nt) {
         leave();
+        unit += s.kt1 - s.c.kt;
         return true;
       }
       const int pos = s.pos0 + min(tok, s.n_tok - 1);
@@ -529,31 +581,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescaled = false;
         uint64_t acc2 = 0ull;
+        // 8 bits: the scales of this key tile (K's already in log2 units)
+        [[maybe_unused]] const uint32_t ksc = base + C::OFF_SCALE + (C::QUANT ? unit % (C::SD + !C::QUANT) : 0) * 1024, vsc = ksc + 512;
+        ++unit;
         auto tile = [&](auto masked_c) {
           constexpr bool kMasked = decltype(masked_c)::value;
           auto xval = [&](const uint32_t* v, int q4, int e) -> float {
             const float x = __uint_as_float(v[e]);
             return (!kMasked || q4 * 32 + e < nvis) ? x : -INFINITY;
           };
-          uint32_t va[32], vb[32];
-          tmem_ld32(tS, va);
+          uint32_t v[4][32];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) tmem_ld32_async(tS + q4 * 32, v[q4]);
+          tmem_wait_ld32(v[0]);
+#pragma unroll
+          for (int q4 = 1; q4 < 4; ++q4) tie32(v[q4]);
+          if constexpr (C::QUANT) {  // logits in place
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const uint4 f = lds128(ksc + (q4 * 32 + e) * 4);
+                const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) mul2(v[q4][e + c], v[q4][e + c + 1], w[c], w[c + 1]);
+              }
+          }
           float mxs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t(&v)[32] = (q4 & 1) ? vb : va;
-            uint32_t(&vn)[32] = (q4 & 1) ? va : vb;
-            tmem_ld32_async(tS + ((q4 + 1) & 3) * 32, vn);
+          for (int q4 = 0; q4 < 4; ++q4)
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              mxs[0] = fmax3(mxs[0], xval(v, q4, e), xval(v, q4, e + 1));
-              mxs[1] = fmax3(mxs[1], xval(v, q4, e + 2), xval(v, q4, e + 3));
-              mxs[2] = fmax3(mxs[2], xval(v, q4, e + 4), xval(v, q4, e + 5));
-              mxs[3] = fmax3(mxs[3], xval(v, q4, e + 6), xval(v, q4, e + 7));
-            }
-            tmem_wait_ld32(vn);
-          }
+            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mxs[c] = fmax3(mxs[c], xval(v[q4], q4, e + 2 * c), xval(v[q4], q4, e + 2 * c + 1));
           const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3]));
-          const float mt = mx * P.scale_log2;
+          const float mt = C::QUANT ? mx : mx * P.scale_log2;
           const bool need = mt > m_use + kMoveReference;
           if (need) {
             alpha = ex2_approx(m_use - mt);
@@ -564,26 +626,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mref = m_use == -INFINITY ? 0.f : m_use;
           const uint64_t negm2 = f2_pack(-mref, -mref);
           uint64_t accq[2] = {0ull, 0ull};
-#pragma unroll 1
-          for (int qq = 0; qq < 4; qq += 2)
 #pragma unroll
-            for (int qi = 0; qi < 2; ++qi) {
-              const int q4 = qq + qi;
-              uint32_t(&v)[32] = qi ? vb : va;
-              uint32_t(&vn)[32] = qi ? va : vb;
-              if (q4 < 3) tmem_ld32_async(tS + (q4 + 1) * 32, vn);
-              uint32_t pk[16];
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t pk[16];
+            [[maybe_unused]] uint4 vs;
 #pragma unroll
-              for (int e2 = 0; e2 < 16; ++e2) {
-                float t0, t1;
-                f2_unpack(f2_fma(f2_pack(xval(v, q4, 2 * e2), xval(v, q4, 2 * e2 + 1)), scale2, negm2), t0, t1);
-                const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                accq[e2 & 1] = f2_add(accq[e2 & 1], f2_pack(p0, p1));
-                pk[e2] = pack_bf16x2(p0, p1);
+            for (int e2 = 0; e2 < 16; ++e2) {
+              float t0, t1;
+              const uint64_t x2 = f2_pack(xval(v[q4], q4, 2 * e2), xval(v[q4], q4, 2 * e2 + 1));
+              f2_unpack(C::QUANT ? f2_add(x2, negm2) : f2_fma(x2, scale2, negm2), t0, t1);
+              float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+              accq[e2 & 1] = f2_add(accq[e2 & 1], f2_pack(p0, p1));
+              if constexpr (C::QUANT) {
+                if ((e2 & 1) == 0) vs = lds128(vsc + (q4 * 32 + 2 * e2) * 4);
+                const uint32_t s0 = (e2 & 1) ? vs.z : vs.x, s1 = (e2 & 1) ? vs.w : vs.y;
+                f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(__uint_as_float(s0), __uint_as_float(s1))), p0, p1);
+                if (kMasked) {  // the scale of a key that is not seen may be anything
+                  if (q4 * 32 + 2 * e2 >= nvis) p0 = 0.f;
+                  if (q4 * 32 + 2 * e2 + 1 >= nvis) p1 = 0.f;
+                }
               }
-              tmem_st16(tS + q4 * 16, pk);
-              if (q4 < 3) tmem_wait_ld32(vn);
+              pk[e2] = pack_bf16x2(p0, p1);
             }
+            tmem_st16(tS + q4 * 16, pk);
+          }
           acc2 = f2_add(accq[0], accq[1]);
         };
         if (masked) tile(std::true_type{});
@@ -611,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool valid = tok < s.n_tok;
       const bool whole = s.c.kt == 0 && s.kt1 == s.units;
-      const bool odd = s.kt1 * 128 > s.pos0 && odd_flag[i % 3] != 0;
+      const bool odd = !C::QUANT && s.kt1 * 128 > s.pos0 && odd_flag[i % 3] != 0;
       const uint32_t* oc = odd_cols + (i % 3) * D;
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that saw no key: zeros
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(P.out.data) + (int64_t)(s.tok0 + min(tok, s.n_tok - 1)) * P.out.ts +
@@ -701,7 +767,12 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
     const int box = 1 << (p.page_log2 < 7 ? p.page_log2 : 7);
     if (!make_tile_map(&km, p.k_pages, rows, D, box) || !make_tile_map(&vm, p.v_pages, rows, D, box)) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(paged_chunk<D, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  // The register split counts on 128 registers a thread at launch: with fewer it would wait for ever.
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, paged_chunk<D, CODE>);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs <= 120) return cudaErrorInvalidKernelImage;
+  e = cudaFuncSetAttribute(paged_chunk<D, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   paged_chunk<D, CODE><<<kPagedCtas, kThreads, C::SMEM, st>>>(P, km, vm);
   count_launches(1);

@@ -96,8 +96,7 @@ class Layer:
     def check(self, got, q, rows=None):
         """got against the fp64 result.  The bound, with u = 2^-8 for bf16 and 2^-24 for f32:
         u |out|    the result's rounding
-        bf16:      u A for the probabilities' rounding and, for 8-bit pools, u A + u B for rows rounded to bf16
-                   (a logit's error d moves its weight by the factor 1 + d: B's definition)
+        bf16:      u A for the probabilities' rounding (8-bit pools: with the value row's scale in them; codes are exact)
         (n + D + 64) 2^-23 (A + |out|) + (D + 8) 2^-23 B   fp32 sums over n keys and D products, exponentials
         (twice the unit roundoff for every operation: tensor cores truncate)."""
         bd = {}
@@ -108,7 +107,7 @@ class Layer:
         n = max(n for n, _ in self.lens)
         tol = u * W + (n + self.D + 64) * 2.0 ** -23 * (A + W) + (self.D + 8) * 2.0 ** -23 * B
         if bf16:
-            tol = tol + u * A + (u * (A + B) if self.quantised else 0)
+            tol = tol + u * A
         sel = np.zeros(self.rows, bool)
         sel[self.starts[0]:self.starts[-1]] = True
         if rows is not None:
