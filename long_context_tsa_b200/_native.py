@@ -349,7 +349,7 @@ class PagedCache:
     float32 ``k_scales`` / ``v_scales`` [n_pages, Hkv, page_size].  All contiguous and on one device.  The buffers
     are referenced, not copied: lengths and table entries are changed in place between calls."""
 
-    __slots__ = ("_tensors", "_c", "_shape", "device")
+    __slots__ = ("_tensors", "_c", "_shape", "_index", "device")
 
     def __init__(self, k_pages, v_pages, page_table, seq_len, token_start, k_scales=None, v_scales=None):
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
@@ -370,6 +370,7 @@ class PagedCache:
             raise ValueError("page_table must be [n_seqs, max_pages], seq_len [n_seqs], token_start [n_seqs + 1]")
         self._tensors = (k_pages, v_pages, k_scales, v_scales, page_table, seq_len, token_start)
         self.device = k_pages.device
+        self._index = k_pages.get_device()  # -1: host memory
         for t in self._tensors:
             if t is not None and (not t.is_contiguous() or t.device != self.device):
                 raise ValueError("the cache's tensors must be contiguous and on one device")
@@ -398,33 +399,37 @@ def alloc_paged_workspace(desc: TsaPagedDesc, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _rows(t: torch.Tensor, desc: TsaPagedDesc, heads: int, device) -> TsaRows:
-    if t.shape != (desc.n_tokens, heads, desc.D) or _DTYPES.get(t.dtype) != desc.dtype or t.stride(2) != 1:
+def _rows(t: torch.Tensor, desc: TsaPagedDesc, heads: int, index: int) -> TsaRows:
+    stride = t.stride()
+    if t.shape != (desc.n_tokens, heads, desc.D) or _DTYPES.get(t.dtype) != desc.dtype or stride[2] != 1:
         raise ValueError(f"expected packed rows [{desc.n_tokens}, {heads}, {desc.D}] of the layer's type with unit last stride")
-    if t.device != device:
-        raise ValueError(f"tensor on {t.device}, cache on {device}")
-    return TsaRows(t.data_ptr(), t.stride(0), t.stride(1))
+    if t.get_device() != index:
+        raise ValueError(f"tensor on {t.device}, cache on device {index}")
+    return TsaRows(t.data_ptr(), stride[0], stride[1])
 
 
 def _paged_call(name: str, desc, cache, a, b, heads: int, ws, stream):
+    # A decoding step makes this call for every layer: the checks are kept to a few hundred ns each.
+    index = cache._index
     if cache._shape != (desc.n_pages, desc.Hkv, desc.page_size, desc.D, desc.cache_dtype, desc.n_seqs, desc.max_pages):
         raise ValueError(f"{name}: the cache's buffers do not have the shape that desc says")
-    device = cache.device
-    ra, rb = _rows(a, desc, heads, device), _rows(b, desc, heads, device)
-    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    ra, rb = _rows(a, desc, heads, index), _rows(b, desc, heads, index)
+    if ws.get_device() != index or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"{name}: the workspace must be contiguous uint8 on the cache's device")
-    if device.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
+    if index < 0:
+        raise ValueError(f"{name}: tensors must be on a CUDA device, got {cache.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    stream = getattr(stream, "cuda_stream", stream)
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    f = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == index:
         code = f(desc, cache._c, ra, rb, ws.data_ptr(), ws.numel(), stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             code = f(desc, cache._c, ra, rb, ws.data_ptr(), ws.numel(), stream)
-    _check(code, name)
+    if code != 0:
+        raise TsaError(code, name)
 
 
 def tsa_cache_write(desc, cache, k, v, ws, stream=None):
