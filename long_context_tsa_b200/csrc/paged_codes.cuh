@@ -77,6 +77,15 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
   return y;
 }
 
+// bf16x2 of the codes in bytes 0 and 2, and in bytes 1 and 3.
+template <int CODE>
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
+  return CODE == kI8 ? i8_pair(w) : e4m3_pair(w << 8);
+}
+template <int CODE>
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
+  return CODE == kI8 ? i8_pair(w >> 8) : e4m3_pair(w);
+}
 // bf16x2 of the codes in bytes i and i + 1 of w (i = 0 or 2).
 template <int CODE, int I>
 __device__ __forceinline__ uint32_t codes_next(uint32_t w) {

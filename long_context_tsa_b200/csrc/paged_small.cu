@@ -47,23 +47,27 @@ using namespace tc;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
-constexpr int kKeys = 16;               // keys of a warp in a unit of 128
+constexpr int kKeys = 16;               // keys of a block: one stage of a warp's ring
 constexpr float kMoveReference = 8.f;   // log2 units
 constexpr uint32_t kDrainPolls = 1u << 26;
 
 template <int D, int CODE, int MT>
 struct Cfg {
   static constexpr int ESZ = CODE == kPlain ? 2 : 1;
+  static constexpr int NB = CODE == kPlain ? 1 : 2;      // blocks of a step
+  static constexpr int KT_LOG2 = CODE == kPlain ? 7 : 8;  // a unit: a step of each warp
+  static constexpr bool QSM = MT == 2;                   // Q fragments in shared memory
   static constexpr int KV_BYTES = kKeys * D * ESZ;       // K or V of 16 keys
   static constexpr int STAGE = 2 * KV_BYTES;
-  static constexpr int RING = (CODE == kPlain ? 192 : 160) * 1024 / kWarps;  // bytes of a warp's ring: what the join leaves
+  static constexpr int RING = (CODE == kPlain && MT == 1 ? 192 : 160) * 1024 / kWarps;  // bytes of a warp's ring: what the rest leaves
   static constexpr int NS = RING / STAGE > 8 ? 8 : RING / STAGE;
   static constexpr int ROWS = 16 * MT;
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_JOIN = kWarps * NS * STAGE;   // 4 partial tiles of 16 rows
   static constexpr int OFF_SCALE = OFF_JOIN + 4 * 16 * D * 4;
   static constexpr int SCALE_BYTES = CODE == kPlain ? 0 : kWarps * NS * 2 * kKeys * 4;
-  static constexpr int OFF_ML = OFF_SCALE + SCALE_BYTES;  // [8 warps][ROWS][m, l]
+  static constexpr int OFF_Q = OFF_SCALE + SCALE_BYTES;  // [MT][D / 16][32 lanes] 16 bytes
+  static constexpr int OFF_ML = OFF_Q + (QSM ? MT * (D / 16) * 512 : 0);  // [8 warps][ROWS][m, l]
   static constexpr int OFF_BAR = OFF_ML + kWarps * ROWS * 8;
   static constexpr int OFF_PLAN = OFF_BAR + kWarps * NS * 8;
   static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanSmem);
@@ -153,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = sbase + C::OFF_RING + warp * C::NS * C::STAGE;
   const uint32_t sscale = sbase + C::OFF_SCALE + warp * C::NS * (2 * kKeys * 4);
   const uint32_t bar = sbase + C::OFF_BAR + warp * C::NS * 8;
+  [[maybe_unused]] const uint32_t sq = sbase + C::OFF_Q;
 
   if (lane == 0) {
     for (int s = 0; s < C::NS; ++s) mbar_init(bar + 8 * s, 1);
@@ -169,16 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long l_left = left;
   int l_keys = P.plan.keys(lc.span, lc.j), l_units = P.plan.units(lc.span, lc.j);
   uint32_t issued = 0, l_stage = 0;  // blocks loaded so far
+  int l_b = 0;                       // block of the step
   int l_entry = 0;                   // page table entry of the next block, read one block ahead
+  auto l_key = [&]() { return (lc.kt << C::KT_LOG2) + (warp * C::NB + l_b) * kKeys; };
   auto l_lookup = [&]() {
-    const int key0 = (lc.kt << 7) + warp * kKeys;
+    const int key0 = l_key();
     if (l_left > 0 && key0 < l_keys) l_entry = __ldg(p.table + (size_t)lc.s * p.max_pages + (key0 >> p.page_log2));
   };
   l_lookup();
-  // Steps over units without keys of this warp; loads one block if there is one.
+  // Steps over blocks without keys; loads one block if there is one.
   auto load_next = [&]() {
     while (l_left > 0) {
-      const int key0 = (lc.kt << 7) + warp * kKeys;
+      const int key0 = l_key();
       const bool has = key0 < l_keys;
       if (has) {
         const int page = checked_page(p, l_entry);
@@ -203,11 +210,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++issued;
         l_stage = l_stage + 1 == C::NS ? 0 : l_stage + 1;
       }
-      --l_left;
-      if (++lc.kt >= l_units && l_left > 0) {
-        plan_next(p, P.plan, &lc);
-        l_keys = P.plan.keys(lc.span, lc.j);
-        l_units = P.plan.units(lc.span, lc.j);
+      if (++l_b == C::NB) {
+        l_b = 0;
+        --l_left;
+        if (++lc.kt >= l_units && l_left > 0) {
+          plan_next(p, P.plan, &lc);
+          l_keys = P.plan.keys(lc.span, lc.j);
+          l_units = P.plan.units(lc.span, lc.j);
+        }
       }
       l_lookup();
       if (has) return;
@@ -230,34 +240,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_rows = n_tok << p.g_log2;
 
     // Queries as A fragments: thread (rg, qj) holds rows rg, rg + 8 at the d of its k indices.
-    uint32_t qa[MT][C::NKS][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    auto q_row = [&](int r) {
+      r = min(r, n_rows - 1);
+      return static_cast<const __nv_bfloat16*>(P.q.data) + (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
+             (int64_t)(cur.g * p.G + (r & (p.G - 1))) * P.q.hs;
+    };
+    auto q_frag = [&](int mt, int ks, uint32_t (&f)[4]) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int r = min(mt * 16 + rg + 8 * hf, n_rows - 1);
-        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(P.q.data) +
-                                  (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
-                                  (int64_t)(cur.g * p.G + (r & (p.G - 1))) * P.q.hs;
+        const __nv_bfloat16* qr = q_row(mt * 16 + rg + 8 * hf);
         if constexpr (CODE == kPlain) {
-#pragma unroll
-          for (int ks = 0; ks < C::NKS; ++ks) {
-            qa[mt][ks][hf] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * qj));
-            qa[mt][ks][hf + 2] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * qj));
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)  // 16 codes of a piece: four k steps of four
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(qr + 64 * h + 16 * qj + 8 * x));
-              qa[mt][4 * h + 2 * x][hf] = v.x;
-              qa[mt][4 * h + 2 * x][hf + 2] = v.y;
-              qa[mt][4 * h + 2 * x + 1][hf] = v.z;
-              qa[mt][4 * h + 2 * x + 1][hf + 2] = v.w;
-            }
+          f[hf] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * qj));
+          f[hf + 2] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * qj));
+        } else {  // the four codes of a word: bytes 0, 2 are one pair of the contraction, bytes 1, 3 the other
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(qr + 64 * (ks >> 2) + 16 * qj + 4 * (ks & 3)));
+          f[hf] = __byte_perm(v.x, v.y, 0x5410);
+          f[hf + 2] = __byte_perm(v.x, v.y, 0x7632);
         }
       }
+    };
+    uint32_t qa[C::QSM ? 1 : MT][C::QSM ? 1 : C::NKS][4];
+    if constexpr (C::QSM) {
+#pragma unroll 1
+      for (int i = warp; i < MT * C::NKS; i += kWarps) {
+        uint32_t f[4];
+        q_frag(i / C::NKS, i % C::NKS, f);
+        st_shared_v4(sq + i * 512 + lane * 16, f[0], f[1], f[2], f[3]);
+      }
+      __syncthreads();  // the previous tile's readers have passed the barriers of its join
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ks = 0; ks < C::NKS; ++ks) q_frag(mt, ks, qa[mt][ks]);
+    }
+    auto frag = [&](int mt, int ks, uint32_t (&f)[4]) {
+      if constexpr (C::QSM) {
+        const uint4 x = lds128(sq + (mt * C::NKS + ks) * 512 + lane * 16);
+        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = qa[mt][ks][e];
+      }
+    };
     int rpos[MT][2];  // position of the thread's rows: they see keys up to it
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -277,13 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
     for (int kt = cur.kt; kt < kt1; ++kt) {
-      const int key0 = (kt << 7) + warp * kKeys;
+      const int key0 = (kt << C::KT_LOG2) + warp * C::NB * kKeys;
       if (key0 >= keys) break;  // later units have none either
+      const bool two = C::NB == 2 && key0 + kKeys < keys;  // a second block was loaded (else its place holds any codes)
+      const uint32_t stage1 = stage + 1 == C::NS ? 0 : stage + 1, phase1 = stage1 == 0 ? phase ^ 1 : phase;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * stage, phase, P.wait_limit, nullptr));
+      if (ok && two) ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * stage1, phase1, P.wait_limit, nullptr));
       if (!ok) break;
       const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::KV_BYTES;
+      [[maybe_unused]] const uint32_t kb[2] = {sk, ring + stage1 * C::STAGE};
+      [[maybe_unused]] const uint32_t sb[2] = {sscale + stage * 128, sscale + stage1 * 128};
       // Rows hide keys behind their own position; keys from `keys` on are not of this sequence.
-      const bool border = key0 + kKeys - 1 > pos0;
+      const bool border = key0 + C::NB * kKeys - 1 > pos0;
 
       if (CODE == kPlain && border) {
         // Values that some row must not see: clear what lies behind the tile's last key, and
@@ -331,12 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
 
-      // ---- S = Q K^T over 16 keys: two column tiles of 8
-      float s[MT][2][4];
+      // ---- S = Q K^T: two column tiles of 8 keys in each block
+      constexpr int NT = 2 * C::NB;
+      float s[MT][NT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
       if constexpr (CODE == kPlain) {
@@ -348,42 +379,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           ldsm4(b, sk + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            mma16816(s[mt][0], qa[mt][ks], b[0], b[1]);
-            mma16816(s[mt][1], qa[mt][ks], b[2], b[3]);
+            uint32_t a[4];
+            frag(mt, ks, a);
+            mma16816(s[mt][0], a, b[0], b[1]);
+            mma16816(s[mt][1], a, b[2], b[3]);
           }
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = 8 * n + O::key(rg);
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t w[NT][4];
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            uint32_t addr;
-            if (D == 128) addr = sk + key * 128 + (((4 * h + qj) ^ (key & 7)) << 4);
-            else addr = sk + (key >> 1) * 128 + ((((key & 1) * 4 + qj) ^ ((key >> 1) & 7)) << 4);
+          for (int n = 0; n < NT; ++n) {
+            const int key = 8 * (n & 1) + O::key(rg);
+            uint32_t addr = kb[n >> 1];
+            if (D == 128) addr += key * 128 + (((4 * h + qj) ^ (key & 7)) << 4);
+            else addr += (key >> 1) * 128 + ((((key & 1) * 4 + qj) ^ ((key >> 1) & 7)) << 4);
             const uint4 v = lds128(addr);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            w[n][0] = v.x, w[n][1] = v.y, w[n][2] = v.z, w[n][3] = v.w;
+          }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = codes_next<CODE, 0>(w[x]), b1 = codes_next<CODE, 2>(w[x]);
+          for (int x = 0; x < 4; ++x) {
+            uint32_t a[MT][4];
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][n], qa[mt][4 * h + x], b0, b1);
+            for (int mt = 0; mt < MT; ++mt) frag(mt, 4 * h + x, a[mt]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t b0 = codes_even<CODE>(w[n][x]), b1 = codes_odd<CODE>(w[n][x]);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][n], a[mt], b0, b1);
             }
           }
         }
       }
 
       // ---- softmax: columns 2 qj, 2 qj + 1 of each column tile
-      float vs[2][2];
+      [[maybe_unused]] float vs[NT][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int key = 8 * n + O::key(2 * qj + e);
           float f = P.scale_log2;
           if constexpr (CODE != kPlain) {
-            f *= lds32(sscale + stage * 128 + 4 * key);
-            vs[n][e] = lds32(sscale + stage * 128 + 64 + 4 * key);
+            f *= lds32(sb[n >> 1] + 4 * (key & 15));
+            vs[n][e] = lds32(sb[n >> 1] + 64 + 4 * (key & 15));
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -401,7 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          mx[mt][hf] = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]), fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+          mx[mt][hf] = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
+#pragma unroll
+          for (int n = 1; n < NT; ++n) mx[mt][hf] = fmax3(mx[mt][hf], s[mt][n][2 * hf], s[mt][n][2 * hf + 1]);
           move |= mx[mt][hf] > m[mt][hf] + kMoveReference;
         }
       if (__any_sync(0xffffffffu, move)) {
@@ -425,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       }
-      uint32_t pa[MT][4];
+      uint32_t pa[C::NB][MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];  // no key seen yet: 2^-inf = 0
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < NT; ++n) {
             float p0 = ex2_approx(s[mt][n][2 * hf] - ref), p1 = ex2_approx(s[mt][n][2 * hf + 1] - ref);
             l[mt][hf] += p0 + p1;
             if constexpr (CODE != kPlain) {
@@ -443,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (s[mt][n][2 * hf + 1] == -INFINITY) p1 = 0.f;
               }
             }
-            pa[mt][2 * n + hf] = pack_bf16x2(p0, p1);
+            pa[n >> 1][mt][2 * (n & 1) + hf] = pack_bf16x2(p0, p1);
           }
         }
 
@@ -457,47 +499,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           ldsm4_t(b, sv + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            mma16816(o[mt][2 * i], pa[mt], b[0], b[1]);
-            mma16816(o[mt][2 * i + 1], pa[mt], b[2], b[3]);
+            mma16816(o[mt][2 * i], pa[0][mt], b[0], b[1]);
+            mma16816(o[mt][2 * i + 1], pa[0][mt], b[2], b[3]);
           }
         }
       } else {
-        uint32_t w[4][D / 32];  // the thread's four keys, D / 8 columns each
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = 8 * (x >> 1) + O::key(2 * qj + (x & 1));
-          if constexpr (D == 128) {
-            const uint4 v = lds128(sv + key * 128 + ((O::piece(rg) ^ (key & 7)) << 4));
-            w[x][0] = v.x;
-            w[x][1] = v.y;
-            w[x][2] = v.z;
-            w[x][3] = v.w;
-          } else {
-            const uint2 v = lds64(sv + (key >> 1) * 128 + ((((key & 1) * 4 + (rg >> 1)) ^ ((key >> 1) & 7)) << 4) + (rg & 1) * 8);
-            w[x][0] = v.x;
-            w[x][1] = v.y;
+        for (int k = 0; k < C::NB; ++k) {
+          const uint32_t svk = kb[k] + C::KV_BYTES;
+          uint32_t w[4][D / 32];  // the thread's four keys, D / 8 columns each
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = 8 * (x >> 1) + O::key(2 * qj + (x & 1));
+            if constexpr (D == 128) {
+              const uint4 v = lds128(svk + key * 128 + ((O::piece(rg) ^ (key & 7)) << 4));
+              w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+            } else {
+              const uint2 v = lds64(svk + (key >> 1) * 128 + ((((key & 1) * 4 + (rg >> 1)) ^ ((key >> 1) & 7)) << 4) + (rg & 1) * 8);
+              w[x][0] = v.x, w[x][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t b[4][2] = {
+                {codes_across<CODE, 0>(w[0][i], w[1][i]), codes_across<CODE, 0>(w[2][i], w[3][i])},
+                {codes_across<CODE, 1>(w[0][i], w[1][i]), codes_across<CODE, 1>(w[2][i], w[3][i])},
+                {codes_across<CODE, 2>(w[0][i], w[1][i]), codes_across<CODE, 2>(w[2][i], w[3][i])},
+                {codes_across<CODE, 3>(w[0][i], w[1][i]), codes_across<CODE, 3>(w[2][i], w[3][i])}};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
           }
         }
+      }
+      __syncwarp();  // every lane has read the stages before they are filled again
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t b[4][2] = {
-              {codes_across<CODE, 0>(w[0][i], w[1][i]), codes_across<CODE, 0>(w[2][i], w[3][i])},
-              {codes_across<CODE, 1>(w[0][i], w[1][i]), codes_across<CODE, 1>(w[2][i], w[3][i])},
-              {codes_across<CODE, 2>(w[0][i], w[1][i]), codes_across<CODE, 2>(w[2][i], w[3][i])},
-              {codes_across<CODE, 3>(w[0][i], w[1][i]), codes_across<CODE, 3>(w[2][i], w[3][i])}};
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * i + x], pa[mt], b[x][0], b[x][1]);
+      for (int k = 0; k < C::NB; ++k) {
+        if (k == 1 && !two) break;
+        ++used;
+        if (++stage == C::NS) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      __syncwarp();  // every lane has read the stage before it is filled again
-      ++used;
-      if (++stage == C::NS) {
-        stage = 0;
-        phase ^= 1;
-      }
       load_next();
+      if (two) load_next();
     }
 
     // ------------------------------------------------ join the warps' parts
@@ -614,7 +661,7 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
   P.out = out;
   P.parts = make_parts(base, C::ROWS, kPagedCtas, D);
   P.plan.which = which;
-  P.plan.kt_log2 = 7;
+  P.plan.kt_log2 = C::KT_LOG2;
   P.plan.tt_log2 = (MT == 2 ? 5 : 4) - p.g_log2;
   P.scale_log2 = p.scale * 1.4426950408889634f;
   P.wait_limit = wait_limit();
