@@ -35,8 +35,8 @@ tsa_status check_paged_desc(const tsa_paged_desc* desc, Paged* p) {
     return TSA_ERR_UNSUPPORTED;
   if (desc->n_seqs > kPagedMaxSeqs) return TSA_ERR_UNSUPPORTED;
   constexpr long long lim = 1LL << 31;
-  if ((long long)desc->n_tokens * desc->Hq >= lim || (long long)desc->max_pages * desc->page_size >= lim)
-    return TSA_ERR_UNSUPPORTED;
+  if ((long long)desc->n_tokens * desc->Hq >= lim || (long long)desc->max_pages * desc->page_size >= lim / 2)
+    return TSA_ERR_UNSUPPORTED;  // positions of a whole tile behind the last one still fit 31 bits
   if ((long long)desc->n_pages * desc->Hkv >= lim || (long long)desc->n_pages * desc->Hkv * desc->page_size >= lim)
     return TSA_ERR_UNSUPPORTED;
   p->T = desc->n_tokens;

@@ -139,14 +139,6 @@ __device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, uint32_t x, uint3
 // registers; 256 x 184 + 256 x 72 is exactly that, and both sides run this before anything else.
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 static_assert(256 * (kSoftmaxRegs + kOtherRegs) <= kThreads * 128, "registers of the block");
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 __device__ __forceinline__ bool any_odd(uint32_t w) { return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0; }
 

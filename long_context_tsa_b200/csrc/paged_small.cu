@@ -45,31 +45,36 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = 8;
-constexpr int kKeys = 16;               // keys of a block: one stage of a warp's ring
+constexpr int kWarps = 8;        // working warps
+constexpr int kLoaders = 4;      // loading warps
+constexpr int kWork = 32 * kWarps;
+constexpr int kThreads = kWork + 32 * kLoaders;
+// Register split: 384 threads x 168 at launch; 256 x 224 + 128 x 56 is exactly that.
+constexpr int kWorkRegs = 224, kLoadRegs = 56;
+static_assert(kWork * kWorkRegs + 128 * kLoadRegs <= kThreads * 168, "registers of the block");
+constexpr int kKeys = 16;               // keys of a block: a warp's part of a stage
+constexpr int kStageKeys = kKeys * kWarps;
 constexpr float kMoveReference = 8.f;   // log2 units
-constexpr uint32_t kDrainPolls = 1u << 26;
+constexpr uint32_t kDrainPolls = 1u << 20;
 
 template <int D, int CODE, int MT>
 struct Cfg {
   static constexpr int ESZ = CODE == kPlain ? 2 : 1;
-  static constexpr int NB = CODE == kPlain ? 1 : 2;      // blocks of a step
-  static constexpr int KT_LOG2 = CODE == kPlain ? 7 : 8;  // a unit: a step of each warp
+  static constexpr int NB = CODE == kPlain ? 1 : 2;      // stages of a step: a block of each for every warp
+  static constexpr int KT_LOG2 = CODE == kPlain ? 7 : 8;  // keys of a step: the unit of the work split
   static constexpr bool QSM = MT == 2;                   // Q fragments in shared memory
-  static constexpr int KV_BYTES = kKeys * D * ESZ;       // K or V of 16 keys
-  static constexpr int STAGE = 2 * KV_BYTES;
-  static constexpr int RING = (CODE == kPlain && MT == 1 ? 192 : 160) * 1024 / kWarps;  // bytes of a warp's ring: what the rest leaves
+  static constexpr int KV_BYTES = kStageKeys * D * ESZ;  // K or V of a stage
+  static constexpr int SC_BYTES = CODE == kPlain ? 0 : 2 * kStageKeys * 4;
+  static constexpr int STAGE = 2 * KV_BYTES + SC_BYTES;
+  static constexpr int RING = (CODE == kPlain && MT == 1 ? 192 : 170) * 1024;  // what the rest leaves
   static constexpr int NS = RING / STAGE > 8 ? 8 : RING / STAGE;
   static constexpr int ROWS = 16 * MT;
   static constexpr int OFF_RING = 0;
-  static constexpr int OFF_JOIN = kWarps * NS * STAGE;   // 4 partial tiles of 16 rows
-  static constexpr int OFF_SCALE = OFF_JOIN + 4 * 16 * D * 4;
-  static constexpr int SCALE_BYTES = CODE == kPlain ? 0 : kWarps * NS * 2 * kKeys * 4;
-  static constexpr int OFF_Q = OFF_SCALE + SCALE_BYTES;  // [MT][D / 16][32 lanes] 16 bytes
+  static constexpr int OFF_JOIN = NS * STAGE;            // 4 partial tiles of 16 rows
+  static constexpr int OFF_Q = OFF_JOIN + 4 * 16 * D * 4;  // [MT][D / 16][32 lanes] 16 bytes
   static constexpr int OFF_ML = OFF_Q + (QSM ? MT * (D / 16) * 512 : 0);  // [8 warps][ROWS][m, l]
   static constexpr int OFF_BAR = OFF_ML + kWarps * ROWS * 8;
-  static constexpr int OFF_PLAN = OFF_BAR + kWarps * NS * 8;
+  static constexpr int OFF_PLAN = OFF_BAR + 2 * NS * 8 + 16;  // full and empty barriers, abort flag
   static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanSmem);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   static constexpr int NKS = D / 16;  // k steps of QK
@@ -154,13 +159,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   PlanSmem* psm = reinterpret_cast<PlanSmem*>(smem + C::OFF_PLAN);
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
   float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
-  const uint32_t ring = sbase + C::OFF_RING + warp * C::NS * C::STAGE;
-  const uint32_t sscale = sbase + C::OFF_SCALE + warp * C::NS * (2 * kKeys * 4);
-  const uint32_t bar = sbase + C::OFF_BAR + warp * C::NS * 8;
+  auto bar_full = [&](uint32_t st) { return sbase + C::OFF_BAR + 8 * st; };
+  auto bar_empty = [&](uint32_t st) { return sbase + C::OFF_BAR + 8 * (C::NS + st); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 2 * C::NS * 8);
   [[maybe_unused]] const uint32_t sq = sbase + C::OFF_Q;
 
-  if (lane == 0) {
-    for (int s = 0; s < C::NS; ++s) mbar_init(bar + 8 * s, 1);
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < C::NS; ++st) {
+      mbar_init(bar_full(st), kLoaders);
+      mbar_init(bar_empty(st), kWarps);
+    }
+    *abort_flag = 0;
     fence_mbar_init();
   }
   Cursor cur;
@@ -169,66 +178,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) P.parts.meta[blockIdx.x].c_end = -1;
   if (left == 0) return;
 
-  // ---- loads: a cursor of their own, up to NS blocks ahead of the products.
-  Cursor lc = cur;
-  long long l_left = left;
-  int l_keys = P.plan.keys(lc.span, lc.j), l_units = P.plan.units(lc.span, lc.j);
-  uint32_t issued = 0, l_stage = 0;  // blocks loaded so far
-  int l_b = 0;                       // block of the step
-  int l_entry = 0;                   // page table entry of the next block, read one block ahead
-  auto l_key = [&]() { return (lc.kt << C::KT_LOG2) + (warp * C::NB + l_b) * kKeys; };
-  auto l_lookup = [&]() {
-    const int key0 = l_key();
-    if (l_left > 0 && key0 < l_keys) l_entry = __ldg(p.table + (size_t)lc.s * p.max_pages + (key0 >> p.page_log2));
-  };
-  l_lookup();
-  // Steps over blocks without keys; loads one block if there is one.
-  auto load_next = [&]() {
-    while (l_left > 0) {
-      const int key0 = l_key();
-      const bool has = key0 < l_keys;
-      if (has) {
-        const int page = checked_page(p, l_entry);
-        const size_t row = (((size_t)page * p.Hkv + lc.g) << p.page_log2) + (key0 & ((1 << p.page_log2) - 1));
-        const uint32_t dst = ring + l_stage * C::STAGE, b = bar + 8 * l_stage;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(b, C::STAGE + (CODE == kPlain ? 0 : 2 * kKeys * 4));
+  if (warp >= kWarps) {
+    // ------------------------------------------------------------ loads
+    // A copy for each page of a stage (128 keys at most), and each costs its warp some 80 clocks: K and
+    // V, and the stage's halves, are different warps'.  Lane i has copy i of its warp; the page of a
+    // copy is looked up a stage ahead.
+    regs_dec<kLoadRegs>();
+    const int box_log2 = min(p.page_log2, 7), box = 1 << box_log2;
+    const int copies = kStageKeys >> box_log2, part = (copies + 1) >> 1;
+    const bool is_v = (warp & 1) != 0;
+    const int at = ((warp >> 1) & 1) * part + lane;  // this lane's copy
+    const bool has_copy = lane < part && at < copies;
+    uint32_t n = 0, st = 0, ph = 1;  // stages so far; next stage; parity that its release has
+    bool good = true;
+    while (left > 0) {
+      const int keys = P.plan.keys(cur.span, cur.j), units = P.plan.units(cur.span, cur.j);
+      const int kt1 = (int)min((long long)units, cur.kt + left);
+      const int end = (int)min((long long)keys, (long long)kt1 << C::KT_LOG2);
+      auto lookup = [&](int key) -> int {
+        return has_copy && key < end ? __ldg(p.table + (size_t)cur.s * p.max_pages + (key >> p.page_log2)) : 0;
+      };
+      int key = (cur.kt << C::KT_LOG2) + (at << box_log2);
+      int entry = lookup(key);
+      for (int key0 = cur.kt << C::KT_LOG2; key0 < end && good; key0 += kStageKeys, key += kStageKeys) {
+        const int next = lookup(key + kStageKeys);
+        const bool mine = has_copy && key < end;
+        const size_t row = (((size_t)(mine ? checked_page(p, entry) : 0) * p.Hkv + cur.g) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        if (n >= C::NS) good = __all_sync(0xffffffffu, mbar_wait(bar_empty(st), ph, P.wait_limit, abort_flag));
+        if (!good) break;
+        const uint32_t full = bar_full(st);
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box * (D * C::ESZ + (CODE == kPlain ? 0 : 4)));
+        __syncwarp();
+        if (mine) {
+          const uint32_t dst = sbase + C::OFF_RING + st * C::STAGE + (is_v ? C::KV_BYTES : 0);
           if constexpr (CODE == kPlain) {
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * 2048, &kmap, b, h * 64, (int)row);
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + C::KV_BYTES + h * 2048, &vmap, b, h * 64, (int)row);
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_2d(dst + h * (kStageKeys * 128) + ((at << box_log2) * 128), is_v ? &vmap : &kmap, full, h * 64, (int)row);
           } else {  // rows of 128 bytes: one key (D = 128) or two (D = 64)
-            const int y = (int)(D == 128 ? row : row >> 1);
-            tma_load_2d(dst, &kmap, b, 0, y);
-            tma_load_2d(dst + C::KV_BYTES, &vmap, b, 0, y);
-            bulk_load(sscale + l_stage * 128, p.k_scales + row, 64, b);
-            bulk_load(sscale + l_stage * 128 + 64, p.v_scales + row, 64, b);
+            tma_load_2d(dst + (at << box_log2) * D, is_v ? &vmap : &kmap, full, 0, (int)(D == 128 ? row : row >> 1));
+            bulk_load(sbase + C::OFF_RING + st * C::STAGE + 2 * C::KV_BYTES + (is_v ? kStageKeys * 4 : 0) + (at << box_log2) * 4,
+                      (is_v ? p.v_scales : p.k_scales) + row, box * 4, full);
           }
         }
         __syncwarp();
-        ++issued;
-        l_stage = l_stage + 1 == C::NS ? 0 : l_stage + 1;
-      }
-      if (++l_b == C::NB) {
-        l_b = 0;
-        --l_left;
-        if (++lc.kt >= l_units && l_left > 0) {
-          plan_next(p, P.plan, &lc);
-          l_keys = P.plan.keys(lc.span, lc.j);
-          l_units = P.plan.units(lc.span, lc.j);
+        ++n;
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
         }
+        entry = next;
       }
-      l_lookup();
-      if (has) return;
+      if (!good) break;
+      left -= kt1 - cur.kt;
+      if (left > 0) plan_next(p, P.plan, &cur);
     }
-  };
-#pragma unroll 1
-  for (int i = 0; i < C::NS; ++i) load_next();
+    if (!good) {
+      record_status(p.status, TSA_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // The last copies must land before the CTA exits, and after an abort nobody else waits for them.
+    for (uint32_t k = n > C::NS ? n - C::NS : 0; k < n; ++k) mbar_wait(bar_full(k % C::NS), (k / C::NS) & 1, kDrainPolls, nullptr);
+    return;
+  }
+  regs_inc<kWorkRegs>();
 
-  uint32_t used = 0, stage = 0, phase = 0;
+  uint32_t stage = 0, phase = 0;
   bool ok = true;
   const int tt = 1 << P.plan.tt_log2;
+  auto work_sync = [&]() { named_sync(1u, kWork); };
 
   while (left > 0) {
     // ------------------------------------------------ one tile of rows, or a part of it
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_frag(i / C::NKS, i % C::NKS, f);
         st_shared_v4(sq + i * 512 + lane * 16, f[0], f[1], f[2], f[3]);
       }
-      __syncthreads();  // the previous tile's readers have passed the barriers of its join
+      work_sync();  // the previous tile's readers have passed the barriers of its join
     } else {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -302,18 +321,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
     for (int kt = cur.kt; kt < kt1; ++kt) {
-      const int key0 = (kt << C::KT_LOG2) + warp * C::NB * kKeys;
-      if (key0 >= keys) break;  // later units have none either
-      const bool two = C::NB == 2 && key0 + kKeys < keys;  // a second block was loaded (else its place holds any codes)
+      if (kt << C::KT_LOG2 >= keys) break;  // a tile that sees nothing
+      const int key0 = (kt << C::KT_LOG2) + warp * kKeys;
+      const bool two = C::NB == 2 && (kt << C::KT_LOG2) + kStageKeys < keys;  // a second stage (else its place holds any codes)
       const uint32_t stage1 = stage + 1 == C::NS ? 0 : stage + 1, phase1 = stage1 == 0 ? phase ^ 1 : phase;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * stage, phase, P.wait_limit, nullptr));
-      if (ok && two) ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * stage1, phase1, P.wait_limit, nullptr));
-      if (!ok) break;
-      const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::KV_BYTES;
-      [[maybe_unused]] const uint32_t kb[2] = {sk, ring + stage1 * C::STAGE};
-      [[maybe_unused]] const uint32_t sb[2] = {sscale + stage * 128, sscale + stage1 * 128};
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, P.wait_limit, abort_flag));
+      if (ok && two) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(stage1), phase1, P.wait_limit, abort_flag));
+      if (!ok) {
+        *abort_flag = 1;
+        break;
+      }
+      if (key0 < keys) {
+      const uint32_t st0 = sbase + C::OFF_RING + stage * C::STAGE, st1 = sbase + C::OFF_RING + stage1 * C::STAGE;
+      const uint32_t sk = st0 + warp * (C::KV_BYTES / (D * C::ESZ / 128 > 1 ? 2 : 1) / kWarps), sv = sk + C::KV_BYTES;
+      [[maybe_unused]] const uint32_t kb[2] = {sk, st1 + (sk - st0)};
+      [[maybe_unused]] const uint32_t sb[2] = {st0 + 2 * C::KV_BYTES + warp * kKeys * 4, st1 + 2 * C::KV_BYTES + warp * kKeys * 4};
       // Rows hide keys behind their own position; keys from `keys` on are not of this sequence.
-      const bool border = key0 + C::NB * kKeys - 1 > pos0;
+      const bool border = key0 + (C::NB - 1) * kStageKeys + kKeys - 1 > pos0;
 
       if (CODE == kPlain && border) {
         // Values that some row must not see: clear what lies behind the tile's last key, and
@@ -323,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kKeys * D * 2 / 512; ++i) {
           const int at = i * 32 + lane;            // 16-byte piece: row, piece
           const int row = at / (D / 8), pc = at % (D / 8);
-          const uint32_t addr = sv + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
+          const uint32_t addr = sv + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
           if (key0 + row >= keys) {
             st_shared_v4(addr, 0u, 0u, 0u, 0u);
           } else if (key0 + row > pos0) {
@@ -340,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (key0 + row <= pos0 || key0 + row >= keys) continue;
 #pragma unroll
             for (int nt = 0; nt < C::NNT; ++nt) {  // the two columns 8 nt + 2 qj of this thread's accumulators
-              const uint32_t addr = sv + (nt >> 3) * 2048 + row * 128 + (((nt & 7) ^ (row & 7)) << 4) + 4 * qj;
+              const uint32_t addr = sv + (nt >> 3) * (kStageKeys * 128) + row * 128 + (((nt & 7) ^ (row & 7)) << 4) + 4 * qj;
               const uint32_t w = __float_as_uint(lds32(addr));
               const float x0 = bf16_lo(w), x1 = bf16_hi(w);
               const bool b0 = !(fabsf(x0) < INFINITY), b1 = !(fabsf(x1) < INFINITY);
@@ -376,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ks = 0; ks < C::NKS; ++ks) {
           const int pc = 2 * ks + half;
           uint32_t b[4];
-          ldsm4(b, sk + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+          ldsm4(b, sk + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];
@@ -419,11 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int key = 8 * n + O::key(2 * qj + e);
+          const int in_block = 8 * (n & 1) + O::key(2 * qj + e), key = (n >> 1) * kStageKeys + in_block;
           float f = P.scale_log2;
           if constexpr (CODE != kPlain) {
-            f *= lds32(sb[n >> 1] + 4 * (key & 15));
-            vs[n][e] = lds32(sb[n >> 1] + 64 + 4 * (key & 15));
+            f *= lds32(sb[n >> 1] + 4 * in_block);
+            vs[n][e] = lds32(sb[n >> 1] + kStageKeys * 4 + 4 * in_block);
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -496,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < D / 16; ++i) {
           const int pc = 2 * i + (lane >> 4);
           uint32_t b[4];
-          ldsm4_t(b, sv + (pc >> 3) * 2048 + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+          ldsm4_t(b, sv + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             mma16816(o[mt][2 * i], pa[0][mt], b[0], b[1]);
@@ -533,18 +557,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      }
       __syncwarp();  // every lane has read the stages before they are filled again
 #pragma unroll
       for (int k = 0; k < C::NB; ++k) {
         if (k == 1 && !two) break;
-        ++used;
+        if (lane == 0) mbar_arrive(bar_empty(stage));
         if (++stage == C::NS) {
           stage = 0;
           phase ^= 1;
         }
       }
-      load_next();
-      if (two) load_next();
     }
 
     // ------------------------------------------------ join the warps' parts
@@ -559,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
         if (qj == 0) ml[warp * C::ROWS + mt * 16 + rg + 8 * hf] = make_float2(m[mt][hf], l[mt][hf]);
       }
-    __syncthreads();
+    work_sync();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       float f[2];
@@ -581,15 +604,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) = o[mt][nt][e] * f[e >> 1];
       }
-      __syncthreads();
+      work_sync();
       if (warp < 4) {
 #pragma unroll
         for (int nt = 0; nt < C::NNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) += o[mt][nt][e] * f[e >> 1];
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 16 * D / 4; i += kThreads) {
+      work_sync();
+      for (int i = threadIdx.x; i < 16 * D / 4; i += kWork) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         const int row = mt * 16 + r;
         if (row >= n_rows) continue;
@@ -626,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      __syncthreads();
+      work_sync();
     }
     if (threadIdx.x == 0 && cur.kt == 0 && kt1 < units) {
       PartMeta mt;
@@ -640,16 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (left > 0) plan_next(p, P.plan, &cur);
   }
 
-  if (!ok && lane == 0) {  // a wait ran out: no copy may still be writing when the CTA exits
-    record_status(p.status, TSA_ERR_TIMEOUT);
-    for (; used != issued; ++used) {
-      mbar_wait(bar + 8 * stage, phase, kDrainPolls, nullptr);
-      if (++stage == C::NS) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
-  }
+  if (!ok && lane == 0) record_status(p.status, TSA_ERR_TIMEOUT);
 }
 
 template <int D, int CODE, int MT>
@@ -667,11 +681,17 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
   P.wait_limit = wait_limit();
   const uint64_t rows = ((uint64_t)p.n_pages * p.Hkv) << p.page_log2;
   CUtensorMap km, vm;
-  const bool made = CODE == kPlain ? make_tile_map(&km, p.k_pages, rows, D, kKeys) && make_tile_map(&vm, p.v_pages, rows, D, kKeys)
-                                   : make_code_map(&km, p.k_pages, rows * D / 128, kKeys * D / 128) &&
-                                         make_code_map(&vm, p.v_pages, rows * D / 128, kKeys * D / 128);
+  const int box = 1 << (p.page_log2 < 7 ? p.page_log2 : 7);
+  const bool made = CODE == kPlain ? make_tile_map(&km, p.k_pages, rows, D, box) && make_tile_map(&vm, p.v_pages, rows, D, box)
+                                   : make_code_map(&km, p.k_pages, rows * D / 128, box * D / 128) &&
+                                         make_code_map(&vm, p.v_pages, rows * D / 128, box * D / 128);
   if (!made) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(paged_small<D, CODE, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  // The register split counts on 168 registers a thread at launch: with fewer it would wait for ever.
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, paged_small<D, CODE, MT>);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs <= 160) return cudaErrorInvalidKernelImage;
+  e = cudaFuncSetAttribute(paged_small<D, CODE, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   paged_small<D, CODE, MT><<<kPagedCtas, kThreads, C::SMEM, st>>>(P, km, vm);
   count_launches(1);
