@@ -58,22 +58,28 @@ __device__ __forceinline__ float code_quotient(float x, float a, float r) {
   return t;
 }
 
+// (a & b) | c in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 // Two bytes of `w` (at bits 0-7 and 16-23; the rest is ignored) as int8 -> bf16x2.
 // With the low seven bits in the mantissa of 128 .. 255, code + 128 (or + 256
 // where the sign is set) is a bf16 number, and the difference is exact.
 __device__ __forceinline__ uint32_t i8_pair(uint32_t w) {
-  const uint32_t a = (w & 0x007f007fu) | 0x43004300u;  // 128 + low bits
-  const uint32_t b = (w & 0x00800080u) | 0x43004300u;  // 128, or 256 for a negative code
+  const uint32_t a = and_or(w, 0x007f007fu, 0x43004300u);  // 128 + low bits
+  const uint32_t b = and_or(w, 0x00800080u, 0xC300C300u);  // -128, or -256 for a negative code
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0x3F803F80u), "r"(b));
   return r;
 }
 // Two bytes at bits 8-15 and 24-31 as e4m3 -> bf16x2: the fields shifted into
 // place give the value times 2^-120 (bias 127 against 7), subnormals included.
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
-  const uint32_t r = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  const uint32_t r = and_or(w, 0x80008000u, (w >> 4) & 0x07f007f0u);
   uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(r), "r"(0x7B807B80u));  // 2^120
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(r), "r"(0x7B807B80u), "r"(0x80008000u));  // times 2^120
   return y;
 }
 
