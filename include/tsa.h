@@ -359,7 +359,7 @@ TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t wi
  *         one, say, where a batch is padded) are neither read nor written.
  *
  * Supported: D 64 or 128; G = Hq / Hkv in {1, 2, 4, 8, 16}; dtype TSA_F32 or
- * TSA_BF16; page_size a power of two from 16 to 1024; n_seqs <= 1024;
+ * TSA_BF16; page_size a power of two from 16 to 1024; n_seqs, Hkv <= 1024;
  * n_tokens * Hq < 2^31; n_pages * Hkv * page_size < 2^31;
  * max_pages * page_size < 2^30.  max_new is the largest number of new tokens of
  * a sequence: it chooses the kernels and the workspace's size; results do not

@@ -33,7 +33,7 @@ tsa_status check_paged_desc(const tsa_paged_desc* desc, Paged* p) {
   if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16) return TSA_ERR_UNSUPPORTED;
   if (desc->page_size < 16 || desc->page_size > 1024 || (desc->page_size & (desc->page_size - 1)) != 0)
     return TSA_ERR_UNSUPPORTED;
-  if (desc->n_seqs > kPagedMaxSeqs) return TSA_ERR_UNSUPPORTED;
+  if (desc->n_seqs > kPagedMaxSeqs || desc->Hkv > kMaxGroups) return TSA_ERR_UNSUPPORTED;
   constexpr long long lim = 1LL << 31;
   if ((long long)desc->n_tokens * desc->Hq >= lim || (long long)desc->max_pages * desc->page_size >= lim / 2)
     return TSA_ERR_UNSUPPORTED;  // positions of a whole tile behind the last one still fit 31 bits

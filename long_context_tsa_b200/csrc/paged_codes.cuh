@@ -34,7 +34,7 @@ __device__ __forceinline__ float code_quotient(float x, float a, float r) {
   constexpr float M = code_max<CODE>();
   const float p = x * M;
   const float t0 = p * r;
-  float t = fmaf(fmaf(-t0, a, p), r, t0);
+  float t = fmaf(-fmaf(t0, a, -p), r, t0);  // in this form a zero keeps its sign
   if (WIDE) {
     float b;
     bool close;

@@ -73,7 +73,7 @@ INV, UNS, WSP = (N.STATUS[f"TSA_ERR_{x}"] for x in ("INVALID_ARG", "UNSUPPORTED"
     (dict(n_tokens=0), INV), (dict(n_seqs=0), INV), (dict(Hq=30), INV), (dict(dtype=N.TSA_I8), INV), (dict(dtype=-1), INV),
     (dict(cache_dtype=N.TSA_F32), INV), (dict(cache_dtype=9), INV), (dict(scale=float("nan")), INV), (dict(max_new=0), INV),
     (dict(max_pages=0), INV), (dict(n_pages=0), INV), (dict(D=96), UNS), (dict(Hq=256), UNS), (dict(Hq=24), UNS),
-    (dict(page_size=8), UNS), (dict(page_size=48), UNS), (dict(page_size=2048), UNS), (dict(n_seqs=1025), UNS),
+    (dict(page_size=8), UNS), (dict(page_size=48), UNS), (dict(page_size=2048), UNS), (dict(n_seqs=1025), UNS), (dict(Hq=1025, Hkv=1025), UNS),
     (dict(n_tokens=1 << 26), UNS), (dict(n_pages=1 << 22), UNS), (dict(max_pages=1 << 25), UNS), (dict(n_pages=0x7fffffff), UNS),
 ])
 def test_bad_shapes(name, kw, code):
