@@ -12,11 +12,12 @@
 //   warps 0-3, 4-7  softmax and epilogue of M tile 0 / 1 (thread = TMEM lane = row)
 //   warps 8-11      preparation: Q tiles (16-byte copies into the swizzled layout);
 //                   8-bit codes -> bf16 K/V tiles; the tiles at the causal border
-//   warp 12         MMA issuer (one thread): S_t = Q_t K^T, O_t += P_t V
+//   warps 12, 14    MMA issuers (one thread) of M tile 0 / 1: S_t = Q_t K^T, O_t += P_t V
 //   warp 13         loads: one TMA box or bulk copy for each page of a tile, issued
 //                   by as many lanes
-// TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D); P_t (bf16)
-// overwrites the first 64 columns of S_t.
+// A step is half a key tile, 64 keys.  TMEM: for each M tile two buffers of 64 columns
+// for S, [0,128) and [128,256); O0 [256,256+D) O1 [256+D,256+2D); P (bf16) overwrites
+// the first 32 columns of its S.
 //
 // 8-bit caches: a value becomes code * scale in fp32 and is rounded to bf16 on
 // its way into the operand tile (relative 2^-9, what tsa_cache_read into bf16
@@ -57,8 +58,9 @@ constexpr int kThreads = 512;
 constexpr int kChunkRows = 256;  // rows of a tile
 constexpr int kPrepWarp0 = 8;
 constexpr int kPrepWarps = 4;
-constexpr int kMmaWarp = 12;
+constexpr int kMmaWarp0 = 12;  // M tile 0; M tile 1: warp 14, on another scheduler
 constexpr int kLoadWarp = 13;
+constexpr int kMmaWarp1 = 14;
 constexpr uint32_t kDrainPolls = 1u << 26;
 constexpr float kMoveReference = 8.0f;  // log2 units
 constexpr uint32_t kNever = 1023;       // "no row": tiles have at most 256 tokens and border keys 383 behind the first
@@ -80,8 +82,8 @@ struct Cfg {
   static constexpr int OFF_SCALE = OFF_RAW + NR * RAW;          // [SD][2][128] floats
   static constexpr int OFF_ODD = OFF_SCALE + SD * 1024;         // [3][D] packed first rows of non-finite values
   static constexpr int OFF_BAR = OFF_ODD + (QUANT ? 0 : 3 * D * 4);
-  // q[2], qfree[2], full[NS], empty[NS], s[2], p[2], o[2], teardown, border[NS] or raw_full[NR], raw_empty[NR]
-  static constexpr int NBAR = 4 + 2 * NS + 6 + 1 + (QUANT ? 2 * NR : NS);
+  // q[2], qfree[2], full[NS], empty[NS], s[4], p[4], o[2], teardown, border[NS] or raw_full[NR], raw_empty[NR]
+  static constexpr int NBAR = 4 + 2 * NS + 10 + 1 + (QUANT ? 2 * NR : NS);
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;           // tmem slot, abort flag, odd[3], done[8]
   static constexpr int OFF_PLAN = (OFF_MISC + 64 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanSmem);
@@ -161,6 +163,7 @@ struct Seg {
   int kt1, units, keys;
   int tok0, n_tok, pos0;  // packed row, tokens and first position of the tile
   int nt;                 // M tiles with rows
+  int nh;                 // steps: halves of key tiles with keys (at least one)
 };
 
 __device__ __forceinline__ Seg make_seg(const ChunkParams& P, const Cursor& c, long long left) {
@@ -174,6 +177,7 @@ __device__ __forceinline__ Seg make_seg(const ChunkParams& P, const Cursor& c, l
   s.n_tok = min(1 << P.plan.tt_log2, c.span.n - first);
   s.pos0 = c.span.base + first;
   s.nt = s.n_tok > (1 << P.rp_log2) ? 2 : 1;
+  s.nh = max(1, min(2 * (s.kt1 - c.kt), (int)(((long long)s.keys + 63) >> 6) - 2 * c.kt));
   return s;
 }
 
@@ -191,14 +195,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_qfree = [&](int t) { return bar0 + 8u * (2 + t); };
   auto bar_full = [&](int s) { return bar0 + 8u * (4 + s); };
   auto bar_empty = [&](int s) { return bar0 + 8u * (4 + C::NS + s); };
-  auto bar_s = [&](int t) { return bar0 + 8u * (4 + 2 * C::NS + t); };
-  auto bar_p = [&](int t) { return bar0 + 8u * (6 + 2 * C::NS + t); };
-  auto bar_o = [&](int t) { return bar0 + 8u * (8 + 2 * C::NS + t); };
-  const uint32_t bar_td = bar0 + 8u * (10 + 2 * C::NS);
+  auto bar_s = [&](int t, int b) { return bar0 + 8u * (4 + 2 * C::NS + 2 * t + b); };
+  auto bar_p = [&](int t, int b) { return bar0 + 8u * (8 + 2 * C::NS + 2 * t + b); };
+  auto bar_o = [&](int t) { return bar0 + 8u * (12 + 2 * C::NS + t); };
+  const uint32_t bar_td = bar0 + 8u * (14 + 2 * C::NS);
   // What the preparing warps wait for: V tiles at the border (by ring stage), or raw tiles.
-  auto bar_border = [&](int s) { return bar0 + 8u * (11 + 2 * C::NS + s); };
-  auto bar_rfull = [&](int s) { return bar0 + 8u * (11 + 2 * C::NS + s); };
-  auto bar_rempty = [&](int s) { return bar0 + 8u * (11 + 2 * C::NS + C::NR + s); };
+  auto bar_border = [&](int s) { return bar0 + 8u * (15 + 2 * C::NS + s); };
+  auto bar_rfull = [&](int s) { return bar0 + 8u * (15 + 2 * C::NS + s); };
+  auto bar_rempty = [&](int s) { return bar0 + 8u * (15 + 2 * C::NS + C::NR + s); };
   uint32_t* odd_cols = reinterpret_cast<uint32_t*>(smem + C::OFF_ODD);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -210,21 +214,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_q(t), 32 * kPrepWarps);
-      mbar_init(bar_s(t), 1);
-      mbar_init(bar_p(t), 128);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar_s(t, b), 1);
+        mbar_init(bar_p(t, b), 128);
+      }
       mbar_init(bar_o(t), 1);
       mbar_init(bar_qfree(t), 1);
     }
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(bar_full(s), kPrepWarps);  // one arrival of each preparing warp, or as many of the loading one
-      mbar_init(bar_empty(s), 1);
+      mbar_init(bar_empty(s), 2);
       if (!C::QUANT) mbar_init(bar_border(s), 1);
     }
     for (int s = 0; s < C::NR; ++s) {
       mbar_init(bar_rfull(s), 1);
       mbar_init(bar_rempty(s), kPrepWarps);
     }
-    mbar_init(bar_td, 1);
+    mbar_init(bar_td, 2);
     *abort_flag = 0;
     odd_flag[0] = odd_flag[1] = odd_flag[2] = 0;
     for (int w = 0; w < 8; ++w) done[w] = 0;
@@ -458,77 +464,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if ((at_border >> st) & 1) mbar_wait(bar_border(st), ((borders >> st) & 1) ^ 1, kDrainPolls, nullptr);
       else mbar_wait(bar_full(st), (k / RING) & 1, kDrainPolls, nullptr);
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    // One thread for both M tiles: their products follow one another whole.  (Two issuing warps,
-    // one for each tile, share the tensor core instruction by instruction, and both tiles' logits
-    // come late: 811 us against 680 for 8192 tokens.)
+  } else if (warp == kMmaWarp0 || warp == kMmaWarp1) {
+    // ------------------------------------------------------------ MMA issuers, one for each M tile
+    // Step u: PV of half u, then QK of half u + 2 into the place that P_u leaves.  The softmax works on
+    // half u + 1 meanwhile, so neither a barrier's latency nor the other M tile's products hold it up.
     if (lane == 0) {
-      constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, 0, 0);
+      const int t = warp == kMmaWarp1;
+      constexpr uint32_t IDESC_QK = idesc_bf16(128, 64, 0, 0);
       constexpr uint32_t IDESC_PV = idesc_bf16(128, D, 0, 1);
       constexpr uint32_t HI = sdesc_hi_sw128(1024);
-      const uint32_t q_lo = sdesc_lo(sQ, 16), k_lo = sdesc_lo(sKV, 16), v_lo = sdesc_lo(sKV, 16384);
+      const uint32_t tS = tmem + t * 128u, tO = tmem + C::O_COL0 + t * D;
+      const uint32_t q_lo = sdesc_lo(sQ + t * C::TILE, 16), k_lo = sdesc_lo(sKV, 16), v_lo = sdesc_lo(sKV, 16384);
       bool ok = true;
-      uint32_t st = 0, ph = 0;  // ring stage and phase of the next tile
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};
-      auto wait_tile = [&](uint32_t stage, uint32_t phase) { return mbar_wait(bar_full(stage), phase, P.wait_limit, abort_flag); };
-      auto next_tile = [&]() {
-        if (++st == C::NS) {
-          st = 0;
+      // Ring stage and phase of the next K and V tile.  A segment's tiles alternate from K on.
+      uint32_t kst = 0, kph = 0, vst = 1, vph = 0;
+      uint32_t pph = 0, nq = 0;  // phases of bar_p by buffer; Q tiles so far
+      auto advance = [&](uint32_t& st, uint32_t& ph) {
+        st += 2;
+        if (st >= (uint32_t)C::NS) {
+          st -= C::NS;
           ph ^= 1;
         }
       };
-      auto qk = [&](int t) {
-        const uint32_t a = q_lo + t * (C::TILE >> 4), b = k_lo + st * (C::TILE >> 4);
+      auto wait_full = [&](uint32_t st, uint32_t ph) { return mbar_wait(bar_full(st), ph, P.wait_limit, abort_flag); };
+      auto qk = [&](int u) {  // half u into its buffer
+        const uint32_t b = k_lo + kst * (C::TILE >> 4) + (u & 1) * 512, d = tS + (u & 1) * 64;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-          if (kk == 0) mma_bf16_ss_lo<false>(tmem + t * 128u, a + off, b + off, HI, IDESC_QK);
-          else mma_bf16_ss_lo<true>(tmem + t * 128u, a + off, b + off, HI, IDESC_QK);
+          if (kk == 0) mma_bf16_ss_lo<false>(d, q_lo + off, b + off, HI, IDESC_QK);
+          else mma_bf16_ss_lo<true>(d, q_lo + off, b + off, HI, IDESC_QK);
         }
+        tc_commit(bar_s(t, u & 1));
       };
       walk([&](const Seg& s, int) -> bool {
-        const int m = s.kt1 - s.c.kt;
-        if (!(ok = wait_tile(st, ph))) return false;
-        for (int t = 0; t < s.nt; ++t) {
-          if (!(ok = mbar_wait(bar_q(t), nq[t]++ & 1, P.wait_limit, abort_flag))) return false;
-          fence_proxy_async_smem();  // rows landed by cp.async are read by the tensor core
-          tc_fence_after();
-          qk(t);
-          tc_commit(bar_s(t));
-          if (m == 1) tc_commit(bar_qfree(t));
+        const int nh = s.nh;
+        // The K tile is done with after its second half, or the last half of all.
+        auto k_done = [&](int u) {
+          if (u & 1 || u == nh - 1) {
+            tc_commit(bar_empty(kst));
+            advance(kst, kph);
+          }
+          if (u == nh - 1) tc_commit(bar_qfree(t));
+        };
+        if (t >= s.nt) {  // no rows here: release the tiles as they come
+          for (int kt = s.c.kt; kt < s.kt1; ++kt) {
+            if (!(ok = wait_full(kst, kph))) return false;
+            mbar_arrive(bar_empty(kst));
+            advance(kst, kph);
+            if (!(ok = wait_full(vst, vph))) return false;
+            mbar_arrive(bar_empty(vst));
+            advance(vst, vph);
+          }
+          return true;
         }
-        tc_commit(bar_empty(st));
-        next_tile();
-        for (int j = 0; j < m; ++j) {
-          if (!(ok = wait_tile(st, ph))) return false;
-          const uint32_t v_st = st;
-          next_tile();  // the next key tile's K
-          for (int t = 0; t < s.nt; ++t) {
-            if (!(ok = mbar_wait(bar_p(t), np[t]++ & 1, P.wait_limit, abort_flag))) return false;
-            tc_fence_after();
-            const uint32_t a = tmem + t * 128u, d = tmem + C::O_COL0 + t * D, b = v_lo + v_st * (C::TILE >> 4);
-            if (j == 0) mma_bf16_ts_lo<false>(d, a, b, HI, IDESC_PV);
-            else mma_bf16_ts_lo<true>(d, a, b, HI, IDESC_PV);
+        if (!(ok = wait_full(kst, kph))) return false;
+        if (!(ok = mbar_wait(bar_q(t), nq++ & 1, P.wait_limit, abort_flag))) return false;
+        fence_proxy_async_smem();  // rows landed by cp.async are read by the tensor core
+        tc_fence_after();
+        for (int u = 0; u < 2 && u < nh; ++u) {
+          qk(u);
+          k_done(u);
+        }
+        for (int u = 0; u < nh; ++u) {
+          if ((u & 1) == 0 && !(ok = wait_full(vst, vph))) return false;
+          if (!(ok = mbar_wait(bar_p(t, u & 1), (pph >> (u & 1)) & 1, P.wait_limit, abort_flag))) return false;
+          pph ^= 1u << (u & 1);
+          tc_fence_after();
+          const uint32_t a = tS + (u & 1) * 64, b = v_lo + vst * (C::TILE >> 4) + (u & 1) * 512;
+          if (u == 0) mma_bf16_ts_lo<false>(tO, a, b, HI, IDESC_PV);
+          else mma_bf16_ts_lo<true>(tO, a, b, HI, IDESC_PV);
 #pragma unroll
-            for (int kk = 1; kk < 8; ++kk) mma_bf16_ts_lo<true>(d, a + kk * 8, b + kk * 128, HI, IDESC_PV);
-            if (j + 1 < m) {
-              if (t == 0) {
-                if (!(ok = wait_tile(st, ph))) return false;
-                tc_fence_after();
-              }
-              qk(t);
-              tc_commit(bar_s(t));
-              if (j + 2 == m) tc_commit(bar_qfree(t));
-            } else {
-              tc_commit(bar_o(t));
+          for (int kk = 1; kk < 4; ++kk) mma_bf16_ts_lo<true>(tO, a + kk * 8, b + kk * 128, HI, IDESC_PV);
+          if (u + 2 < nh) {
+            if ((u & 1) == 0) {
+              if (!(ok = wait_full(kst, kph))) return false;
+              tc_fence_after();
             }
+            qk(u + 2);
+          } else {
+            tc_commit(bar_o(t));  // the last two steps
           }
-          tc_commit(bar_empty(v_st));
-          if (j + 1 < m) {
-            tc_commit(bar_empty(st));
-            next_tile();
+          if (u & 1 || u == nh - 1) {
+            tc_commit(bar_empty(vst));
+            advance(vst, vph);
           }
+          if (u + 2 < nh) k_done(u + 2);
         }
         return true;
       });
@@ -544,12 +565,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + (uint32_t)t * 128u;
+    const uint32_t tS0 = tmem + lane_off + (uint32_t)t * 128u;
     const uint32_t tO = tmem + lane_off + C::O_COL0 + t * D;
     const int hh = r >> P.rp_log2, tok = (t << P.rp_log2) + (r & ((1 << P.rp_log2) - 1));
-    uint32_t ns = 0, no = 0;
+    uint32_t sph = 0, no = 0;  // phases of bar_s by buffer; waits on bar_o
     [[maybe_unused]] uint32_t unit = 0;  // key tiles so far
     bool ok = true;
+    auto wait_o = [&]() {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_o(t), no++ & 1, P.wait_limit, abort_flag));
+      return ok;
+    };
     walk([&](const Seg& s, int i) -> bool {
       auto leave = [&]() {
         __threadfence_block();
@@ -564,33 +589,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = s.pos0 + min(tok, s.n_tok - 1);
       const int last = min(pos + 1, s.keys);  // keys this row sees
       float m_use = -INFINITY, l = 0.f;
-      for (int kt = s.c.kt; kt < s.kt1; ++kt) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s(t), ns++ & 1, P.wait_limit, abort_flag));
+      for (int u = 0; u < s.nh; ++u) {
+        const int buf = u & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_s(t, buf), (sph >> buf) & 1, P.wait_limit, abort_flag));
         if (!ok) return false;
+        sph ^= 1u << buf;
         tc_fence_after();
-        const int nvis = last - kt * 128;
-        const bool masked = __any_sync(0xffffffffu, nvis < 128);
+        const uint32_t tS = tS0 + buf * 64;
+        const int nvis = last - (2 * s.c.kt + u) * 64;
+        const bool masked = __any_sync(0xffffffffu, nvis < 64);
         float alpha = 1.f;
         bool rescaled = false;
         uint64_t acc2 = 0ull;
-        // 8 bits: the scales of this key tile (K's already in log2 units)
-        [[maybe_unused]] const uint32_t ksc = base + C::OFF_SCALE + (C::QUANT ? unit % (C::SD + !C::QUANT) : 0) * 1024, vsc = ksc + 512;
-        ++unit;
+        // 8 bits: the scales of this half (K's already in log2 units)
+        [[maybe_unused]] const uint32_t ksc =
+            base + C::OFF_SCALE + (C::QUANT ? (unit + (u >> 1)) % (C::SD + !C::QUANT) : 0) * 1024 + buf * 256, vsc = ksc + 512;
         auto tile = [&](auto masked_c) {
           constexpr bool kMasked = decltype(masked_c)::value;
           auto xval = [&](const uint32_t* v, int q4, int e) -> float {
             const float x = __uint_as_float(v[e]);
             return (!kMasked || q4 * 32 + e < nvis) ? x : -INFINITY;
           };
-          uint32_t v[4][32];
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) tmem_ld32_async(tS + q4 * 32, v[q4]);
+          uint32_t v[2][32];
+          tmem_ld32_async(tS, v[0]);
+          tmem_ld32_async(tS + 32, v[1]);
           tmem_wait_ld32(v[0]);
-#pragma unroll
-          for (int q4 = 1; q4 < 4; ++q4) tie32(v[q4]);
+          tie32(v[1]);
           if constexpr (C::QUANT) {  // logits in place
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
+            for (int q4 = 0; q4 < 2; ++q4)
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const uint4 f = lds128(ksc + (q4 * 32 + e) * 4);
@@ -601,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float mxs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
+          for (int q4 = 0; q4 < 2; ++q4)
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
 #pragma unroll
@@ -613,13 +640,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             alpha = ex2_approx(m_use - mt);
             m_use = mt;
           }
-          rescaled = kt > s.c.kt && __any_sync(0xffffffffu, need);
+          rescaled = u > 0 && __any_sync(0xffffffffu, need);
           const uint64_t scale2 = f2_pack(P.scale_log2, P.scale_log2);
           const float mref = m_use == -INFINITY ? 0.f : m_use;
           const uint64_t negm2 = f2_pack(-mref, -mref);
           uint64_t accq[2] = {0ull, 0ull};
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
+          for (int q4 = 0; q4 < 2; ++q4) {
             uint32_t pk[16];
             [[maybe_unused]] uint4 vs;
 #pragma unroll
@@ -649,8 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s0, s1;
         f2_unpack(acc2, s0, s1);
         l = l * alpha + (s0 + s1);
-        // O_t is idle: the commit that released this S_t covers the previous PV.
         if (rescaled) {
+          // The previous PV must have finished: the commit of the next S covers it, or the last but one of all.
+          if (u + 1 < s.nh) ok = __all_sync(0xffffffffu, mbar_wait(bar_s(t, buf ^ 1), (sph >> (buf ^ 1)) & 1, P.wait_limit, abort_flag));
+          else wait_o();
+          if (!ok) return false;
+          tc_fence_after();
 #pragma unroll
           for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t v[32];
@@ -662,11 +693,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_p(t));
+        mbar_arrive(bar_p(t, buf));
+        if (u == s.nh - 1 && u > 0 && !rescaled && !wait_o()) return false;  // every phase is waited for
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_o(t), no++ & 1, P.wait_limit, abort_flag));
-      if (!ok) return false;
+      if (!wait_o()) return false;
       tc_fence_after();
+      unit += s.kt1 - s.c.kt;
       const bool valid = tok < s.n_tok;
       const bool whole = s.c.kt == 0 && s.kt1 == s.units;
       const bool odd = !C::QUANT && s.kt1 * 128 > s.pos0 && odd_flag[i % 3] != 0;
