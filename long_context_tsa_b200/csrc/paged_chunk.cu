@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* done = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 20);     // [8]: segments that each softmax warp has left
   PlanSmem* psm = reinterpret_cast<PlanSmem*>(smem + C::OFF_PLAN);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_q(t), 32 * kPrepWarps);
@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuers, one for each M tile
     // Step u: PV of half u, then QK of half u + 2 into the place that P_u leaves.  The softmax works on
     // half u + 1 meanwhile, so neither a barrier's latency nor the other M tile's products hold it up.
-    if (lane == 0) {
+    {
+      const uint32_t on = elect_one();
       const int t = warp == kMmaWarp1;
       constexpr uint32_t IDESC_QK = idesc_bf16(128, 64, 0, 0);
       constexpr uint32_t IDESC_PV = idesc_bf16(128, D, 0, 1);
@@ -486,40 +487,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       };
-      auto wait_full = [&](uint32_t st, uint32_t ph) { return mbar_wait(bar_full(st), ph, P.wait_limit, abort_flag); };
+      auto wait_full = [&](uint32_t st, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar_full(st), ph, P.wait_limit, abort_flag)); };
       auto qk = [&](int u) {  // half u into its buffer
         const uint32_t b = k_lo + kst * (C::TILE >> 4) + (u & 1) * 512, d = tS + (u & 1) * 64;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-          if (kk == 0) mma_bf16_ss_lo<false>(d, q_lo + off, b + off, HI, IDESC_QK);
-          else mma_bf16_ss_lo<true>(d, q_lo + off, b + off, HI, IDESC_QK);
+          if (kk == 0) mma_bf16_ss_lo<false>(on, d, q_lo + off, b + off, HI, IDESC_QK);
+          else mma_bf16_ss_lo<true>(on, d, q_lo + off, b + off, HI, IDESC_QK);
         }
-        tc_commit(bar_s(t, u & 1));
+        tc_commit_on(on, bar_s(t, u & 1));
       };
       walk([&](const Seg& s, int) -> bool {
         const int nh = s.nh;
         // The K tile is done with after its second half, or the last half of all.
         auto k_done = [&](int u) {
           if (u & 1 || u == nh - 1) {
-            tc_commit(bar_empty(kst));
+            tc_commit_on(on, bar_empty(kst));
             advance(kst, kph);
           }
-          if (u == nh - 1) tc_commit(bar_qfree(t));
+          if (u == nh - 1) tc_commit_on(on, bar_qfree(t));
         };
         if (t >= s.nt) {  // no rows here: release the tiles as they come
           for (int kt = s.c.kt; kt < s.kt1; ++kt) {
             if (!(ok = wait_full(kst, kph))) return false;
-            mbar_arrive(bar_empty(kst));
+            if (on) mbar_arrive(bar_empty(kst));
             advance(kst, kph);
             if (!(ok = wait_full(vst, vph))) return false;
-            mbar_arrive(bar_empty(vst));
+            if (on) mbar_arrive(bar_empty(vst));
             advance(vst, vph);
           }
           return true;
         }
         if (!(ok = wait_full(kst, kph))) return false;
-        if (!(ok = mbar_wait(bar_q(t), nq++ & 1, P.wait_limit, abort_flag))) return false;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar_q(t), nq++ & 1, P.wait_limit, abort_flag)))) return false;
         fence_proxy_async_smem();  // rows landed by cp.async are read by the tensor core
         tc_fence_after();
         for (int u = 0; u < 2 && u < nh; ++u) {
@@ -528,14 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int u = 0; u < nh; ++u) {
           if ((u & 1) == 0 && !(ok = wait_full(vst, vph))) return false;
-          if (!(ok = mbar_wait(bar_p(t, u & 1), (pph >> (u & 1)) & 1, P.wait_limit, abort_flag))) return false;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar_p(t, u & 1), (pph >> (u & 1)) & 1, P.wait_limit, abort_flag)))) return false;
           pph ^= 1u << (u & 1);
           tc_fence_after();
           const uint32_t a = tS + (u & 1) * 64, b = v_lo + vst * (C::TILE >> 4) + (u & 1) * 512;
-          if (u == 0) mma_bf16_ts_lo<false>(tO, a, b, HI, IDESC_PV);
-          else mma_bf16_ts_lo<true>(tO, a, b, HI, IDESC_PV);
+          if (u == 0) mma_bf16_ts_lo<false>(on, tO, a, b, HI, IDESC_PV);
+          else mma_bf16_ts_lo<true>(on, tO, a, b, HI, IDESC_PV);
 #pragma unroll
-          for (int kk = 1; kk < 4; ++kk) mma_bf16_ts_lo<true>(tO, a + kk * 8, b + kk * 128, HI, IDESC_PV);
+          for (int kk = 1; kk < 4; ++kk) mma_bf16_ts_lo<true>(on, tO, a + kk * 8, b + kk * 128, HI, IDESC_PV);
           if (u + 2 < nh) {
             if ((u & 1) == 0) {
               if (!(ok = wait_full(kst, kph))) return false;
@@ -543,18 +544,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             qk(u + 2);
           } else {
-            tc_commit(bar_o(t));  // the last two steps
+            tc_commit_on(on, bar_o(t));  // the last two steps
           }
           if (u & 1 || u == nh - 1) {
-            tc_commit(bar_empty(vst));
+            tc_commit_on(on, bar_empty(vst));
             advance(vst, vph);
           }
           if (u + 2 < nh) k_done(u + 2);
         }
         return true;
       });
-      if (!ok) fail();
-      tc_commit(bar_td);  // every MMA has finished before TMEM is released
+      if (!ok && lane == 0) fail();
+      __syncwarp();
+      tc_commit_on(on, bar_td);  // every MMA has finished before TMEM is released
       mbar_wait(bar_td, 0, kDrainPolls, nullptr);
     }
     __syncwarp();
