@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_q(t), 32 * kPrepWarps);
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar_s(t, b), 1);
-        mbar_init(bar_p(t, b), 128);
+        mbar_init(bar_p(t, b), 4);  // the softmax warps of an M tile
       }
       mbar_init(bar_o(t), 1);
       mbar_init(bar_qfree(t), 1);
@@ -528,7 +528,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           k_done(u);
         }
         for (int u = 0; u < nh; ++u) {
-          if ((u & 1) == 0 && !(ok = wait_full(vst, vph))) return false;
+          bool k_ready = true;  // asked before the wait for P, so that the answer is there after it
+          if ((u & 1) == 0) {
+            if (!(ok = wait_full(vst, vph))) return false;
+            k_ready = u + 2 >= nh || __all_sync(0xffffffffu, mbar_test(bar_full(kst), kph));
+          }
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar_p(t, u & 1), (pph >> (u & 1)) & 1, P.wait_limit, abort_flag)))) return false;
           pph ^= 1u << (u & 1);
           tc_fence_after();
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 1; kk < 4; ++kk) mma_bf16_ts_lo<true>(on, tO, a + kk * 8, b + kk * 128, HI, IDESC_PV);
           if (u + 2 < nh) {
-            if ((u & 1) == 0) {
+            if (!k_ready) {
               if (!(ok = wait_full(kst, kph))) return false;
               tc_fence_after();
             }
@@ -591,15 +595,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = s.pos0 + min(tok, s.n_tok - 1);
       const int last = min(pos + 1, s.keys);  // keys this row sees
       float m_use = -INFINITY, l = 0.f;
+      bool s_ready = false;
       for (int u = 0; u < s.nh; ++u) {
         const int buf = u & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s(t, buf), (sph >> buf) & 1, P.wait_limit, abort_flag));
-        if (!ok) return false;
+        if (!s_ready) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_s(t, buf), (sph >> buf) & 1, P.wait_limit, abort_flag));
+          if (!ok) return false;
+        }
         sph ^= 1u << buf;
         tc_fence_after();
         const uint32_t tS = tS0 + buf * 64;
         const int nvis = last - (2 * s.c.kt + u) * 64;
-        const bool masked = __any_sync(0xffffffffu, nvis < 64);
+        const bool masked = (2 * s.c.kt + u) * 64 + 63 > s.pos0;  // some row of the tile does not see all of it
         float alpha = 1.f;
         bool rescaled = false;
         uint64_t acc2 = 0ull;
@@ -638,10 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3]));
           const float mt = C::QUANT ? mx : mx * P.scale_log2;
           const bool need = mt > m_use + kMoveReference;
-          if (need) {
-            alpha = ex2_approx(m_use - mt);
-            m_use = mt;
-          }
+          alpha = need ? ex2_approx(m_use - mt) : 1.f;
+          m_use = need ? mt : m_use;
           rescaled = u > 0 && __any_sync(0xffffffffu, need);
           const uint64_t scale2 = f2_pack(P.scale_log2, P.scale_log2);
           const float mref = m_use == -INFINITY ? 0.f : m_use;
@@ -693,9 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(tO + q4 * 32, v);
           }
         }
+        // The next half's logits are mostly there by now: asking here hides the answer's latency.
+        const bool s_next = u + 1 < s.nh && mbar_test(bar_s(t, buf ^ 1), (sph >> (buf ^ 1)) & 1);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_p(t, buf));
+        s_ready = __all_sync(0xffffffffu, s_next);
+        if (lane == 0) mbar_arrive(bar_p(t, buf));
         if (u == s.nh - 1 && u > 0 && !rescaled && !wait_o()) return false;  // every phase is waited for
       }
       if (!wait_o()) return false;
