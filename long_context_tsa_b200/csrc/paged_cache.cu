@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;  // of a block
-constexpr int kFlight = 2;      // 16-byte loads in flight for each thread; full occupancy hides more than longer flights do
 
 // The row of the pools (head 0) for each of the block's tokens t0 .. t0 + n - 1, or -1.
 // One warp; n <= 32.
@@ -88,6 +87,18 @@ __device__ __forceinline__ void pack_codes(const float (&q)[E], uint32_t (&code)
   }
 }
 
+// a / M, correctly rounded: the product with the correctly rounded 1 / M and one correction by its
+// remainder (Markstein, as for the codes).  a and a / M normal numbers.
+template <int CODE>
+__device__ __forceinline__ float scale_of(float a) {
+  constexpr float M = code_max<CODE>(), r = 1.f / M;
+  const float q = a * r;
+  return fmaf(-fmaf(q, M, -a), r, q);
+}
+
+// A thread has the same piece of a K row and of the V row beside it: one place and one pair of
+// offsets for both, and two loads in flight.  Full occupancy hides more than longer flights do.
+//
 // IN: float or bf16; CODE: kPlain keeps IN.
 template <typename IN, int CODE, int D>
 __global__ void __launch_bounds__(kThreads, 8) cache_write(const Paged p, const Rows k, const Rows v, int tb_log2) {
@@ -95,35 +106,30 @@ __global__ void __launch_bounds__(kThreads, 8) cache_write(const Paged p, const 
   constexpr int LPR = D / E;               // lanes of a row
   __shared__ int rows[kMaxTokens];
   const int t0 = blockIdx.x << tb_log2, n = min(1 << tb_log2, p.T - t0);
-  const int all = (2 * p.Hkv << tb_log2) * LPR;  // pieces of the block
+  const int all = (p.Hkv << tb_log2) * LPR;  // pieces of the block
   const int c = threadIdx.x % LPR;
   check_starts(p);
-  for (int base = 0; base < all; base += kThreads * kFlight) {
-    uint4 x[kFlight];
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int r = (base + i * kThreads + (int)threadIdx.x) / LPR, tok = r & ((1 << tb_log2) - 1), h = r >> tb_log2;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (h < 2 * p.Hkv && tok < n) {  // K heads, then V heads
-        const bool is_v = h >= p.Hkv;
-        const Rows& src = is_v ? v : k;
-        const IN* row = static_cast<const IN*>(src.data) + (int64_t)(t0 + tok) * src.ts + (int64_t)(is_v ? h - p.Hkv : h) * src.hs;
-        x[i] = __ldcs(reinterpret_cast<const uint4*>(row + c * E));
-      }
+  for (int base = 0; base < all; base += kThreads) {
+    const int r = (base + (int)threadIdx.x) / LPR, tok = r & ((1 << tb_log2) - 1), h = r >> tb_log2;
+    const bool live = h < p.Hkv && tok < n;
+    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (live) {
+      const IN* kr = static_cast<const IN*>(k.data) + (int64_t)(t0 + tok) * k.ts + (int64_t)h * k.hs + c * E;
+      const IN* vr = static_cast<const IN*>(v.data) + (int64_t)(t0 + tok) * v.ts + (int64_t)h * v.hs + c * E;
+      x[0] = __ldcs(reinterpret_cast<const uint4*>(kr));
+      x[1] = __ldcs(reinterpret_cast<const uint4*>(vr));
     }
     if (base == 0) {
       if (threadIdx.x < 32) find_rows(p, t0, n, rows);
       __syncthreads();
     }
+    const int at = live ? rows[tok] : -1;
+    const size_t row = (size_t)at + ((size_t)h << p.page_log2);
 #pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      if (base + i * kThreads >= all) break;  // the same for the whole block
-      const int r = (base + i * kThreads + (int)threadIdx.x) / LPR, tok = r & ((1 << tb_log2) - 1), h = r >> tb_log2;
-      const bool is_v = h >= p.Hkv;
-      const int at = h < 2 * p.Hkv && tok < n ? rows[tok] : -1;
-      const size_t row = (size_t)at + ((size_t)(is_v ? h - p.Hkv : h) << p.page_log2);
+    for (int i = 0; i < 2; ++i) {
+      void* pages = i ? p.v_pages : p.k_pages;
       if constexpr (CODE == kPlain) {
-        if (at >= 0) *reinterpret_cast<uint4*>(static_cast<IN*>(is_v ? p.v_pages : p.k_pages) + row * D + c * E) = x[i];
+        if (at >= 0) *reinterpret_cast<uint4*>(static_cast<IN*>(pages) + row * D + c * E) = x[i];
       } else {
         const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         float f[E];
@@ -143,14 +149,14 @@ __global__ void __launch_bounds__(kThreads, 8) cache_write(const Paged p, const 
 #pragma unroll
         for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float a = __uint_as_float(top);
-        float q[E];
-        bool finite = true;
+        float q[E], scale;
         if (E == 8 && __all_sync(0xffffffffu, a > 8.6736174e-19f && a < 1.2676506e30f)) {  // 2^-60, 2^100
-          const float rinv = 1.f / a;
+          const float rinv = rcp_approx(a);
 #pragma unroll
           for (int e = 0; e < E; ++e) q[e] = code_quotient<CODE, false>(f[e], a, rinv);
+          scale = scale_of<CODE>(a);
         } else {
-          finite = top < 0x7f800000u;
+          const bool finite = top < 0x7f800000u;
           // A power of two brings the row to where products and remainders neither over- nor underflow.
           const float two = a > 1.2676506e30f ? 5.4210109e-20f : a < 8.6736174e-19f ? 1.8446744e19f : 1.f;  // 2^-64, 2^64
           const float as = finite ? a * two : 0.f;
@@ -160,14 +166,15 @@ __global__ void __launch_bounds__(kThreads, 8) cache_write(const Paged p, const 
             const float t = code_quotient<CODE, sizeof(IN) == 4>(finite ? fabsf(f[e]) * two : 0.f, as, rinv);
             q[e] = finite ? copysignf(t, f[e]) : 0.f;
           }
+          scale = finite ? a / code_max<CODE>() : __uint_as_float(0x7fffffffu);
         }
         uint32_t code[E / 4];
         pack_codes<CODE, E>(q, code);
         if (at >= 0) {
-          uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + row * D + c * E;
+          uint8_t* dst = static_cast<uint8_t*>(pages) + row * D + c * E;
           if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
           else *reinterpret_cast<uint32_t*>(dst) = code[0];
-          if (c == 0) (is_v ? p.v_scales : p.k_scales)[row] = finite ? a / code_max<CODE>() : __uint_as_float(0x7fffffffu);
+          if (c == 0) (i ? p.v_scales : p.k_scales)[row] = scale;
         }
       }
     }
@@ -179,41 +186,35 @@ template <typename OUT, int CODE, int D>
 __global__ void __launch_bounds__(kThreads, 8) cache_read(const Paged p, const Rows k, const Rows v, int tb_log2) {
   constexpr int E = CODE == kPlain ? 16 / (int)sizeof(OUT) : 8;  // elements of a lane
   constexpr int LPR = D / E;
+  using Raw = typename std::conditional<CODE == kPlain, uint4, uint2>::type;
   __shared__ int rows[kMaxTokens];
   const int t0 = blockIdx.x << tb_log2, n = min(1 << tb_log2, p.T - t0);
-  const int all = (2 * p.Hkv << tb_log2) * LPR;
+  const int all = (p.Hkv << tb_log2) * LPR;
   const int c = threadIdx.x % LPR;
   check_starts(p);
   if (threadIdx.x < 32) find_rows(p, t0, n, rows);
   __syncthreads();
-  for (int base = 0; base < all; base += kThreads * kFlight) {
-    using Raw = typename std::conditional<CODE == kPlain, uint4, uint2>::type;
-    Raw x[kFlight];
-    float scale[kFlight];
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int r = (base + i * kThreads + (int)threadIdx.x) / LPR, tok = r & ((1 << tb_log2) - 1), h = r >> tb_log2;
-      const bool is_v = h >= p.Hkv;
-      const int at = h < 2 * p.Hkv && tok < n ? rows[tok] : -1;
-      const size_t row = (size_t)at + ((size_t)(is_v ? h - p.Hkv : h) << p.page_log2);
-      if (at >= 0) {
-        if constexpr (CODE == kPlain) {
-          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const OUT*>(is_v ? p.v_pages : p.k_pages) + row * D + c * E));
-        } else {
-          x[i] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(is_v ? p.v_pages : p.k_pages) + row * D + c * E));
-          scale[i] = __ldg((is_v ? p.v_scales : p.k_scales) + row);
-        }
-      }
+#pragma unroll 1
+  for (int base = 0; base < all; base += kThreads) {
+    const int r = (base + (int)threadIdx.x) / LPR, tok = r & ((1 << tb_log2) - 1), h = r >> tb_log2;
+    if (h >= p.Hkv || tok >= n) continue;
+    const int at = rows[tok];
+    if (at < 0) continue;
+    const size_t row = (size_t)at + ((size_t)h << p.page_log2), from = row * (D * (CODE == kPlain ? sizeof(OUT) : 1)) + c * sizeof(Raw);
+    Raw x[2];
+    float scale[2];
+    x[0] = __ldg(reinterpret_cast<const Raw*>(static_cast<const char*>(p.k_pages) + from));
+    x[1] = __ldg(reinterpret_cast<const Raw*>(static_cast<const char*>(p.v_pages) + from));
+    if (CODE != kPlain) {
+      scale[0] = __ldg(p.k_scales + row);
+      scale[1] = __ldg(p.v_scales + row);
     }
 #pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int r = (base + i * kThreads + (int)threadIdx.x) / LPR, tok = r & ((1 << tb_log2) - 1), h = r >> tb_log2;
-      if (h >= 2 * p.Hkv || tok >= n || rows[tok] < 0) continue;
-      const bool is_v = h >= p.Hkv;
-      const Rows& dst = is_v ? v : k;
-      OUT* row = static_cast<OUT*>(dst.data) + (int64_t)(t0 + tok) * dst.ts + (int64_t)(is_v ? h - p.Hkv : h) * dst.hs + c * E;
+    for (int i = 0; i < 2; ++i) {
+      const Rows& dst = i ? v : k;
+      OUT* to = static_cast<OUT*>(dst.data) + (int64_t)(t0 + tok) * dst.ts + (int64_t)h * dst.hs + c * E;
       if constexpr (CODE == kPlain) {
-        __stcs(reinterpret_cast<uint4*>(row), x[i]);
+        __stcs(reinterpret_cast<uint4*>(to), x[i]);
       } else {
         const uint32_t y[2] = {x[i].x, x[i].y};
         float f[8];
@@ -226,11 +227,11 @@ __global__ void __launch_bounds__(kThreads, 8) cache_read(const Paged p, const R
           f[4 * e + 3] = bf16_hi(hi) * scale[i];
         }
         if constexpr (sizeof(OUT) == 2) {
-          __stcs(reinterpret_cast<uint4*>(row), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+          __stcs(reinterpret_cast<uint4*>(to), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                          pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
         } else {
-          __stcs(reinterpret_cast<float4*>(row), make_float4(f[0], f[1], f[2], f[3]));
-          __stcs(reinterpret_cast<float4*>(row) + 1, make_float4(f[4], f[5], f[6], f[7]));
+          __stcs(reinterpret_cast<float4*>(to), make_float4(f[0], f[1], f[2], f[3]));
+          __stcs(reinterpret_cast<float4*>(to) + 1, make_float4(f[4], f[5], f[6], f[7]));
         }
       }
     }

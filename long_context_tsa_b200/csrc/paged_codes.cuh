@@ -16,15 +16,24 @@ __device__ __forceinline__ constexpr float code_max() {
   return CODE == kI8 ? 127.f : 448.f;
 }
 
-// |x| M / a for a row whose largest magnitude is a > 0, rounded so that rounding
-// it once more to the code's grid gives what the exact quotient would.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x M / a for a row whose largest magnitude is a > 0, rounded so that rounding
+// it once more to the code's grid gives what the exact quotient would.  r: 1 / a,
+// off by a few units in the last place at most.
 //
-// The quotient is the product with 1 / a and one correction by its remainder
+// The quotient is the product with r and one correction by its remainder
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990): a quotient that fp32 holds, so every tie of a grid of at
-// most 8 bits, comes out exact.  With 8-bit significands (bf16 rows) no other
+// processor", 1990).  The product is off by some 2^-22 of the quotient, the
+// remainder is exact, and its product with r off by 2^-22 again: a quotient that
+// fp32 holds, so every tie of a grid of at most 8 bits, comes out exact, and any
+// other within fp32's rounding.  With 8-bit significands (bf16 rows) no other
 // quotient lies within 2^-16 of a border between two codes, so this decides
-// every case.  fp32 rows can come closer: next to a border b the sign of
+// every case.  fp32 rows (x >= 0) can come closer: next to a border b the sign of
 // x M - b a decides.  Both products are known exactly there: x M as its rounded
 // value and the remainder of the rounding, and x M - b a because b has at most
 // 8 bits and the two agree in at least 12.
