@@ -8,7 +8,7 @@
 // NaN).  Reading gives code * scale in fp32, rounded to the output's type.
 //
 // Both kernels move bytes and nothing bounds them but HBM.  A block takes up to
-// 16 consecutive tokens; its first warp finds their places (in the write kernel
+// 8 consecutive tokens; its first warp finds their places (in the write kernel
 // while the first loads are under way), then all threads walk over the (head,
 // token) rows, tokens first.
 #include <type_traits>
@@ -22,7 +22,7 @@ namespace tsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // of a block
+constexpr int kMaxTokens = 8;  // of a block
 
 // The row of the pools (head 0) for each of the block's tokens t0 .. t0 + n - 1, or -1.
 // One warp; n <= 32.
@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 8) cache_read(const Paged p, const R
 
 template <typename X, int CODE, int D>
 cudaError_t launch(bool write, const Paged& p, const Rows& k, const Rows& v, cudaStream_t st) {
-  // Tokens of a block, as long as that leaves four blocks for every SM.  bf16: 16 (131072 x 8 rows
-  // from e4m3 in 143 us; 4: 157).  f32: 4 (98000 x 8 rows from int8 in 130 us; 16: 150).
-  int tb_log2 = sizeof(X) == 2 ? 4 : 2;
+  // Tokens of a block, as long as that leaves four blocks for every SM.  bf16: 8 (131072 x 8 rows to
+  // int8 and back in 286 us; 4: 297, 16: 294).  f32: 4 (98000 x 8 rows from int8 in 137 us; 2: 164, 8: 147).
+  int tb_log2 = sizeof(X) == 2 ? 3 : 2;
   while (tb_log2 > 0 && (p.T >> tb_log2) < 4 * kPagedCtas) --tb_log2;
   const unsigned blocks = (unsigned)(((long long)p.T + (1 << tb_log2) - 1) >> tb_log2);
   if (write) cache_write<X, CODE, D><<<blocks, kThreads, 0, st>>>(p, k, v, tb_log2);

@@ -10,6 +10,7 @@
 #include "internal.h"
 #include "paged.h"
 #include "paged_codes.cuh"
+#include "paged_plan.cuh"
 
 namespace tsa {
 namespace {
@@ -19,6 +20,7 @@ constexpr int kRows = 8;  // rows of a block
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts parts) {
+  grid_dependency_wait();  // launched while the kernel before still runs
   const PartMeta meta = parts.meta[blockIdx.x];
   if (meta.c_end < 0) return;
   const int first = blockIdx.x, n = min(meta.c_end, parts.ctas - 1) - first + 1;
@@ -64,16 +66,25 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
 }  // namespace
 
 cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st) {
-  const dim3 grid(parts.ctas, (parts.rows + kRows - 1) / kRows);
-  if (p.dtype == TSA_BF16) {
-    if (p.D == 64) paged_combine<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(p, out, parts);
-    else paged_combine<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(p, out, parts);
-  } else {
-    if (p.D == 64) paged_combine<float, 64><<<grid, kThreads, 0, st>>>(p, out, parts);
-    else paged_combine<float, 128><<<grid, kThreads, 0, st>>>(p, out, parts);
-  }
+  // A programmatic launch: the blocks are in place when the kernel that leaves the parts ends.
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts.ctas, (parts.rows + kRows - 1) / kRows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (p.dtype == TSA_BF16)
+    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 64>, p, out, parts)
+                  : cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 128>, p, out, parts);
+  else
+    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<float, 64>, p, out, parts)
+                  : cudaLaunchKernelEx(&cfg, paged_combine<float, 128>, p, out, parts);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace tsa

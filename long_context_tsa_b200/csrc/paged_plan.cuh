@@ -158,6 +158,10 @@ __device__ __forceinline__ void plan_next(const Paged& p, const Plan& pl, Cursor
 
 #ifdef __CUDACC__  // the rest of the header also serves the host checks
 
+// Programmatic launches: the joining kernel may be set up from here on, and waits for this one's end.
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct PlanSmem {
   long long warp_sum[32];
   int s;
@@ -171,6 +175,7 @@ struct PlanSmem {
 template <int THREADS>
 __device__ __forceinline__ void plan_start(const Paged& p, const Plan& pl, PlanSmem* sm, Cursor* cur, long long* left,
                                            long long* run_out) {
+  grid_dependency_launch();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int per = (p.S + THREADS - 1) / THREADS;
   const int s0 = min(p.S, t * per), s1 = min(p.S, s0 + per);
