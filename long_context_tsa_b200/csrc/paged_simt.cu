@@ -106,14 +106,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
     };
     __syncthreads();  // the previous tile's buffers are free
     find_rows(cur.kt);
-    for (int i = tid; i < ROWS * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
+#pragma unroll 4
+    for (int j = 0; j < ROWS * (D / 4) / kThreads; ++j) {
+      const int i = j * kThreads + tid, r = i / (D / 4), c = i % (D / 4) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < n_rows) {
-        const float* g = static_cast<const float*>(P.q.data) + (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
-                     (int64_t)(cur.g * p.G + (r & (p.G - 1))) * P.q.hs + c;
-        x = *reinterpret_cast<const float4*>(g);
-      }
+      if (r < n_rows)
+        x = *reinterpret_cast<const float4*>(static_cast<const float*>(P.q.data) + (int64_t)(cur.span.tok0 + first_tok + (r >> p.g_log2)) * P.q.ts +
+                                             (int64_t)(cur.g * p.G + (r & (p.G - 1))) * P.q.hs + c);
       *reinterpret_cast<float4*>(Qs + r * C::KS + c) = x;
     }
 
@@ -135,19 +134,27 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
       __syncthreads();  // rows found; K and V of the previous tile are done with
       using Pc = Piece<CODE>;
       constexpr int PPR = D / Pc::N;
+      constexpr int N = kKeys * PPR / kThreads, B = N < 4 ? N : 4;  // pieces of a thread; in flight, of K and V each
+#pragma unroll 1
+      for (int i0 = 0; i0 < N; i0 += B) {
+        Pc k[B], v[B];
 #pragma unroll
-      for (int i = tid; i < kKeys * PPR; i += kThreads) {
-        const int n = i / PPR, c = i % PPR * Pc::N;
-        const int r = rows[n];
-        Pc k = {}, v = {};
-        if (r >= 0) {
-          k.load(p.k_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.k_scales + r));
-          v.load(p.v_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.v_scales + r));
+        for (int j = 0; j < B; ++j) {
+          const int i = (i0 + j) * kThreads + tid, c = i % PPR * Pc::N, r = rows[i / PPR];
+          k[j] = v[j] = Pc{};
+          if (r >= 0) {
+            k[j].load(p.k_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.k_scales + r));
+            v[j].load(p.v_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.v_scales + r));
+          }
         }
 #pragma unroll
-        for (int e = 0; e < Pc::N; e += 4) {
-          *reinterpret_cast<float4*>(Ks + n * C::KS + c + e) = make_float4(k.f[e], k.f[e + 1], k.f[e + 2], k.f[e + 3]);
-          *reinterpret_cast<float4*>(Vs + n * D + c + e) = make_float4(v.f[e], v.f[e + 1], v.f[e + 2], v.f[e + 3]);
+        for (int j = 0; j < B; ++j) {
+          const int i = (i0 + j) * kThreads + tid, n = i / PPR, c = i % PPR * Pc::N;
+#pragma unroll
+          for (int e = 0; e < Pc::N; e += 4) {
+            *reinterpret_cast<float4*>(Ks + n * C::KS + c + e) = make_float4(k[j].f[e], k[j].f[e + 1], k[j].f[e + 2], k[j].f[e + 3]);
+            *reinterpret_cast<float4*>(Vs + n * D + c + e) = make_float4(v[j].f[e], v[j].f[e + 1], v[j].f[e + 2], v[j].f[e + 3]);
+          }
         }
       }
       if (kt + 1 < kt1) find_rows(kt + 1);

@@ -60,8 +60,8 @@ constexpr uint32_t kDrainPolls = 1u << 20;
 template <int D, int CODE, int MT>
 struct Cfg {
   static constexpr int ESZ = CODE == kPlain ? 2 : 1;
-  static constexpr int NB = CODE == kPlain ? 1 : 2;      // stages of a step: a block of each for every warp
-  static constexpr int KT_LOG2 = CODE == kPlain ? 7 : 8;  // keys of a step: the unit of the work split
+  static constexpr int NB = CODE == kPlain || MT == 2 ? 1 : 2;      // stages of a step: a block of each for every warp
+  static constexpr int KT_LOG2 = NB == 1 ? 7 : 8;  // keys of a step: the unit of the work split
   static constexpr bool QSM = MT == 2;                   // Q fragments in shared memory
   static constexpr int KV_BYTES = kStageKeys * D * ESZ;  // K or V of a stage
   static constexpr int SC_BYTES = CODE == kPlain ? 0 : 2 * kStageKeys * 4;
