@@ -703,8 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         s_ready = __all_sync(0xffffffffu, s_next);
+        // Every phase of bar_o is waited for before the next can complete: the last but one's needs this P.
+        if (u == s.nh - 1 && u > 0 && !rescaled && !wait_o()) return false;
         if (lane == 0) mbar_arrive(bar_p(t, buf));
-        if (u == s.nh - 1 && u > 0 && !rescaled && !wait_o()) return false;  // every phase is waited for
       }
       if (!wait_o()) return false;
       tc_fence_after();

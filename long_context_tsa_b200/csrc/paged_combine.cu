@@ -17,14 +17,39 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRows = 8;  // rows of a block
+constexpr int kMaxParts = 2 * kPagedCtas;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts parts) {
+  __shared__ float weight[kMaxParts][kRows];  // of each part: 2^(m_i - m)
+  __shared__ float inverse[kRows];
   grid_dependency_wait();  // launched while the kernel before still runs
   const PartMeta meta = parts.meta[blockIdx.x];
   if (meta.c_end < 0) return;
   const int first = blockIdx.x, n = min(meta.c_end, parts.ctas - 1) - first + 1;
   const int rp_log2 = 7 - p.g_log2;
+  auto slot = [&](int k) { return (size_t)(first + k) * 2 + (k == 0 ? 1 : 0); };
+  {  // sixteen lanes for each row
+    const int lr = threadIdx.x / 16, lane = threadIdx.x % 16, row = blockIdx.y * kRows + lr;
+    float top = -INFINITY;
+    for (int k = lane; k < n; k += 16) {
+      const float m = parts.ml[slot(k) * 2 * parts.rows + row];
+      weight[k][lr] = m;
+      top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.f;
+    for (int k = lane; k < n; k += 16) {
+      const float m = weight[k][lr], f = m == top ? 1.f : exp2f(m - top);
+      weight[k][lr] = f;
+      sum += f * parts.ml[(slot(k) * 2 + 1) * parts.rows + row];
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) inverse[lr] = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw no key: zeros
+  }
+  __syncthreads();
   for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
     // Neighbouring threads take neighbouring float4s of the parts' layout.
     const int lr = parts.by_head ? i % kRows : i / (D / 4);
@@ -39,22 +64,18 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
       head = row & (p.G - 1);
     }
     if (tok >= meta.n_tok) continue;
-    auto slot = [&](int k) { return (size_t)(first + k) * 2 + (k == 0 ? 1 : 0); };
-    float top = -INFINITY;
-    for (int k = 0; k < n; ++k) top = fmaxf(top, parts.ml[slot(k) * 2 * parts.rows + row]);
-    float sum = 0.f;
+    const float* src = parts.o + row * parts.row_stride + c4 * parts.c4_stride;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float m = parts.ml[slot(k) * 2 * parts.rows + row];
-      const float f = m == top ? 1.f : exp2f(m - top);
-      sum += f * parts.ml[(slot(k) * 2 + 1) * parts.rows + row];
-      const float4 o = *reinterpret_cast<const float4*>(parts.o + slot(k) * parts.rows * D + row * parts.row_stride + c4 * parts.c4_stride);
+      const float f = weight[k][lr];
+      const float4 o = *reinterpret_cast<const float4*>(src + slot(k) * parts.rows * D);
       a.x += f * o.x;
       a.y += f * o.y;
       a.z += f * o.z;
       a.w += f * o.w;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw no key: zeros
+    const float inv = inverse[lr];
     T* dst = static_cast<T*>(out.data) + (int64_t)(meta.tok0 + tok) * out.ts + (int64_t)(meta.g * p.G + head) * out.hs + c4 * 4;
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<float4*>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);

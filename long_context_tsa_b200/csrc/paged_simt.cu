@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
   constexpr int R = ROWS / 16;  // rows of a thread
   constexpr int K4 = kKeys / 16;
   constexpr int DJ = D / 64;    // float4 columns of a thread
+  constexpr bool kAhead = ROWS == 16;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
   float* Ks = sm + C::OFF_K;
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
     };
     __syncthreads();  // the previous tile's buffers are free
     find_rows(cur.kt);
+    if (kAhead && cur.kt + 1 < kt1) find_rows(cur.kt + 1);
 #pragma unroll 4
     for (int j = 0; j < ROWS * (D / 4) / kThreads; ++j) {
       const int i = j * kThreads + tid, r = i / (D / 4), c = i % (D / 4) * 4;
@@ -128,36 +130,52 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
       for (int j = 0; j < DJ; ++j) o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 
-    for (int kt = cur.kt; kt < kt1; ++kt) {
-      const int key0 = kt * kKeys;
+    using Pc = Piece<CODE>;
+    constexpr int PPR = D / Pc::N, N = kKeys * PPR / kThreads;  // pieces of a row, and of a thread
+    constexpr int B = kAhead || N < 4 ? N : 4;                 // in flight, of K and V each
+    Pc k[B], v[B];
+    auto load = [&](int kt, int i0) {
       const int* rows = rows_of + (kt & 1) * kKeys;
-      __syncthreads();  // rows found; K and V of the previous tile are done with
-      using Pc = Piece<CODE>;
-      constexpr int PPR = D / Pc::N;
-      constexpr int N = kKeys * PPR / kThreads, B = N < 4 ? N : 4;  // pieces of a thread; in flight, of K and V each
-#pragma unroll 1
-      for (int i0 = 0; i0 < N; i0 += B) {
-        Pc k[B], v[B];
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
-          const int i = (i0 + j) * kThreads + tid, c = i % PPR * Pc::N, r = rows[i / PPR];
-          k[j] = v[j] = Pc{};
-          if (r >= 0) {
-            k[j].load(p.k_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.k_scales + r));
-            v[j].load(p.v_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.v_scales + r));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          const int i = (i0 + j) * kThreads + tid, n = i / PPR, c = i % PPR * Pc::N;
-#pragma unroll
-          for (int e = 0; e < Pc::N; e += 4) {
-            *reinterpret_cast<float4*>(Ks + n * C::KS + c + e) = make_float4(k[j].f[e], k[j].f[e + 1], k[j].f[e + 2], k[j].f[e + 3]);
-            *reinterpret_cast<float4*>(Vs + n * D + c + e) = make_float4(v[j].f[e], v[j].f[e + 1], v[j].f[e + 2], v[j].f[e + 3]);
-          }
+      for (int j = 0; j < B; ++j) {
+        const int i = (i0 + j) * kThreads + tid, c = i % PPR * Pc::N, r = rows[i / PPR];
+        k[j] = v[j] = Pc{};
+        if (r >= 0) {
+          k[j].load(p.k_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.k_scales + r));
+          v[j].load(p.v_pages, (size_t)r * D + c, CODE == kPlain ? 1.f : __ldg(p.v_scales + r));
         }
       }
-      if (kt + 1 < kt1) find_rows(kt + 1);
+    };
+    auto store = [&](int i0) {
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const int i = (i0 + j) * kThreads + tid, n = i / PPR, c = i % PPR * Pc::N;
+#pragma unroll
+        for (int e = 0; e < Pc::N; e += 4) {
+          *reinterpret_cast<float4*>(Ks + n * C::KS + c + e) = make_float4(k[j].f[e], k[j].f[e + 1], k[j].f[e + 2], k[j].f[e + 3]);
+          *reinterpret_cast<float4*>(Vs + n * D + c + e) = make_float4(v[j].f[e], v[j].f[e + 1], v[j].f[e + 2], v[j].f[e + 3]);
+        }
+      }
+    };
+    if (kAhead) {
+      __syncthreads();
+      load(cur.kt, 0);
+    }
+    for (int kt = cur.kt; kt < kt1; ++kt) {
+      const int key0 = kt * kKeys;
+      __syncthreads();  // rows found; K and V of the previous tile are done with
+      if constexpr (kAhead) {  // few rows: bound by the loads, so the next tile's are under way during this one's products
+        store(0);
+        if (kt + 1 < kt1) load(kt + 1, 0);
+        if (kt + 2 < kt1) find_rows(kt + 2);
+      } else {
+#pragma unroll 1
+        for (int i0 = 0; i0 < N; i0 += B) {
+          load(kt, i0);
+          store(i0);
+        }
+        if (kt + 1 < kt1) find_rows(kt + 1);
+      }
       __syncthreads();
 
       float s[R][K4];
