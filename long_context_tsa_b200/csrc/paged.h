@@ -68,15 +68,16 @@ inline Parts make_parts(void* base, int rows, int ctas, int D) {
 
 cudaError_t launch_cache_write(const Paged& p, const Rows& k, const Rows& v, cudaStream_t st);
 cudaError_t launch_cache_read(const Paged& p, const Rows& k, const Rows& v, cudaStream_t st);
-// Attention: each launcher takes `parts_base` of at least paged_*_bytes() for the partial tiles.
-size_t paged_simt_bytes(const Paged& p);
-cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* parts_base, cudaStream_t st);
+// Attention: each launcher takes `base` of at least paged_*_bytes() (16-byte aligned) for the
+// partial tiles that it leaves, and says how they lie.
 // which: 0 every sequence, 1 those with at most kSplitRows rows, 2 the others.
+size_t paged_simt_bytes(const Paged& p);
+cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts);
 size_t paged_small_bytes(const Paged& p);
-cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* parts_base, int which, cudaStream_t st);
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts);
 size_t paged_chunk_bytes(const Paged& p);
-cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* parts_base, int which, cudaStream_t st);
-// Joins the partial tiles that a kernel left behind.
-cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st);
+cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts);
+// Joins the partial tiles of one or two kernels (b.ctas = 0: of a alone).
+cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& a, const Parts& b, cudaStream_t st);
 
 }  // namespace tsa

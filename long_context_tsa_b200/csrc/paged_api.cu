@@ -97,20 +97,32 @@ tsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSA_OK : TSA_E
 
 // f32 runs on CUDA cores.  bf16: short sequences go to the kernel for few rows,
 // longer ones to the kernel for chunks; a batch that may hold both kinds takes
-// both, each doing its own.
+// both, each doing its own (a token over a long cache takes the chunk kernel
+// nearly twice as long).
 bool all_short(const Paged& p) { return (long long)p.max_new * p.G <= kSplitRows; }
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t workspace_bytes(const Paged& p) {
   if (p.dtype != TSA_BF16) return kHeaderBytes + paged_simt_bytes(p);
-  return kHeaderBytes + (all_short(p) ? paged_small_bytes(p) : paged_chunk_bytes(p));
+  if (all_short(p)) return kHeaderBytes + paged_small_bytes(p);
+  return kHeaderBytes + paged_chunk_bytes(p) + (p.S > 1 ? 256 + paged_small_bytes(p) : 0);
 }
 
-cudaError_t launch_attend(const Paged& p, const Rows& q, const Rows& out, void* parts, cudaStream_t st) {
-  if (p.dtype != TSA_BF16) return launch_paged_simt(p, q, out, parts, st);
-  if (all_short(p)) return launch_paged_small(p, q, out, parts, 0, st);
-  if (p.S == 1) return launch_paged_chunk(p, q, out, parts, 0, st);
-  const cudaError_t e = launch_paged_small(p, q, out, parts, 1, st);
-  return e != cudaSuccess ? e : launch_paged_chunk(p, q, out, parts, 2, st);
+cudaError_t launch_attend(const Paged& p, const Rows& q, const Rows& out, char* base, cudaStream_t st) {
+  Parts a = {}, b = {};
+  cudaError_t e;
+  if (p.dtype != TSA_BF16) {
+    e = launch_paged_simt(p, q, out, base, st, &a);
+  } else if (all_short(p)) {
+    e = launch_paged_small(p, q, out, base, 0, st, &a);
+  } else if (p.S == 1) {
+    e = launch_paged_chunk(p, q, out, base, 0, st, &a);
+  } else {
+    e = launch_paged_small(p, q, out, base + align256(paged_chunk_bytes(p)), 1, st, &b);
+    if (e == cudaSuccess) e = launch_paged_chunk(p, q, out, base, 2, st, &a);
+  }
+  return e != cudaSuccess ? e : launch_paged_combine(p, out, a, b, st);
 }
 
 // The checks that the three calls share; a and b: the packed tensors.

@@ -20,13 +20,17 @@ constexpr int kRows = 8;  // rows of a block
 constexpr int kMaxParts = 2 * kPagedCtas;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts parts) {
+__global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts pa, const Parts pb) {
   __shared__ float weight[kMaxParts][kRows];  // of each part: 2^(m_i - m)
   __shared__ float inverse[kRows];
   grid_dependency_wait();  // launched while the kernel before still runs
-  const PartMeta meta = parts.meta[blockIdx.x];
+  const bool of_b = (int)blockIdx.x >= pa.ctas;
+  const Parts& parts = of_b ? pb : pa;
+  const int first = blockIdx.x - (of_b ? pa.ctas : 0);
+  if ((int)blockIdx.y * kRows >= parts.rows) return;
+  const PartMeta meta = parts.meta[first];
   if (meta.c_end < 0) return;
-  const int first = blockIdx.x, n = min(meta.c_end, parts.ctas - 1) - first + 1;
+  const int n = min(meta.c_end, parts.ctas - 1) - first + 1;
   const int rp_log2 = 7 - p.g_log2;
   auto slot = [&](int k) { return (size_t)(first + k) * 2 + (k == 0 ? 1 : 0); };
   {  // sixteen lanes for each row
@@ -86,24 +90,25 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
 
 }  // namespace
 
-cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st) {
+cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& a, const Parts& b, cudaStream_t st) {
   // A programmatic launch: the blocks are in place when the kernel that leaves the parts ends.
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(parts.ctas, (parts.rows + kRows - 1) / kRows);
+  const int rows = b.ctas > 0 && b.rows > a.rows ? b.rows : a.rows;
+  cfg.gridDim = dim3(a.ctas + b.ctas, (rows + kRows - 1) / kRows);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.dtype == TSA_BF16)
-    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 64>, p, out, parts)
-                  : cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 128>, p, out, parts);
+    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 64>, p, out, a, b)
+                  : cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 128>, p, out, a, b);
   else
-    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<float, 64>, p, out, parts)
-                  : cudaLaunchKernelEx(&cfg, paged_combine<float, 128>, p, out, parts);
+    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<float, 64>, p, out, a, b)
+                  : cudaLaunchKernelEx(&cfg, paged_combine<float, 128>, p, out, a, b);
   count_launches(1);
   return e;
 }

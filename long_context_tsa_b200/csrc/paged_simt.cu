@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
 int rows_log2(const Paged& p) { return (long long)p.max_new * p.G <= 16 ? 4 : 6; }
 
 template <int CODE, int D, int ROWS>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
   using C = Cfg<D, ROWS>;
   SimtParams P;
   P.p = p;
@@ -316,28 +316,28 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, c
   if (e != cudaSuccess) return e;
   paged_simt<CODE, D, ROWS><<<C::CTAS, kThreads, C::SMEM, st>>>(P);
   count_launches(1);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_paged_combine(p, out, P.parts, st);
+  *parts = P.parts;
+  return cudaGetLastError();
 }
 
 template <int CODE, int D>
-cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st) {
-  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, st) : launch<CODE, D, 64>(p, q, out, base, st);
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
+  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, st, parts) : launch<CODE, D, 64>(p, q, out, base, st, parts);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st) {
-  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, st);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, st);
-  return by_rows<kPlain, D>(p, q, out, base, st);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
+  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, st, parts);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, st, parts);
+  return by_rows<kPlain, D>(p, q, out, base, st, parts);
 }
 
 }  // namespace
 
 size_t paged_simt_bytes(const Paged& p) { return parts_bytes(1 << rows_log2(p), 2 * kPagedCtas, p.D); }
 
-cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* parts_base, cudaStream_t st) {
-  return p.D == 64 ? by_code<64>(p, q, out, parts_base, st) : by_code<128>(p, q, out, parts_base, st);
+cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, st, parts) : by_code<128>(p, q, out, base, st, parts);
 }
 
 }  // namespace tsa

@@ -8,17 +8,27 @@
 // concern, and accumulators in registers need no round trip through TMEM), and
 // everything else serves to keep loads in flight:
 //
-// - The run of key tiles of a CTA (paged_plan.cuh) is cut over its 8 warps, 16
-//   keys of each 128 to a warp.  Warps share nothing until a tile of rows ends:
-//   each has its own ring of TMA boxes (16 keys never cross a page), its own
-//   running reference and sum, its own accumulators.  A warp's ring runs across
-//   the ends of tiles, so loads never pause for the join of a tile.
+// - A CTA, one on each SM, has an equal run of the key tiles (paged_plan.cuh).
+//   Stages of 128 keys go through a ring of TMA boxes, one box a page; each of
+//   the 8 working warps takes 16 keys of a stage and has its own running
+//   reference and sum and its own accumulators, joined when a tile of rows ends.
+//   The ring runs on across the ends of tiles.
+// - Four warps load.  Issuing a copy costs a warp some 80 clocks, so the working
+//   warps must not do it (four 131072-token int8 contexts: 363 us with a loading
+//   lane in each working warp, 287 with loading warps), and a copy covers as much
+//   of a page as a stage holds.
 // - 8-bit codes become bf16 without rounding (both kinds are exact in bf16); the
 //   scale of a key multiplies its logits, the scale of a value its probability,
 //   both in fp32.  Codes are read as whole 16-byte pieces of a row: the order of
 //   the contraction index d, of the 16 keys and of the output columns is free as
 //   long as both operands agree, and is chosen so that a thread's pieces are
-//   contiguous and a quarter warp's fall into different banks.
+//   contiguous, a quarter warp's fall into different banks, and K's codes need no
+//   byte moves.  The conversions (some 4 logic operations for 2 codes) are what
+//   bounds the 8-bit kernels: the ALU pipe is over 70 % busy.
+// - A step of one row tile takes a block of two stages at once for 8-bit caches,
+//   which gives the scheduler two independent halves (241 us against 257); with
+//   two row tiles the registers do not suffice for that (237 us against 217 for
+//   16 x 8 tokens in e4m3).
 // - The reference m of the softmax moves only when a logit passes it by 2^8
 //   (P <= 2^8, bf16's relative precision is the same there), found with one vote
 //   a block; the sum over a row's four threads waits until the tile ends.
@@ -30,6 +40,10 @@
 // row that is not finite and hidden from some row of the tile would still give
 // 0 * inf: where the causal border crosses the 16 keys, non-finite values of an
 // unscaled cache are added to the rows that see them and cleared in the tile.
+//
+// Measured: 61 sequences of up to 8192 tokens, bf16, one token each: 138 us, 5.6
+// TB/s (90 % of a copy's rate with the joining kernel); four of 131072 in int8:
+// 241 us, 4.6 TB/s; 16 of up to 32768 in e4m3, up to 8 tokens each: 217 us, 2.8 TB/s.
 #include <cuda.h>
 #include <math.h>
 
@@ -332,231 +346,231 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if (key0 < keys) {
-      const uint32_t st0 = sbase + C::OFF_RING + stage * C::STAGE, st1 = sbase + C::OFF_RING + stage1 * C::STAGE;
-      const uint32_t sk = st0 + warp * (C::KV_BYTES / (D * C::ESZ / 128 > 1 ? 2 : 1) / kWarps), sv = sk + C::KV_BYTES;
-      [[maybe_unused]] const uint32_t kb[2] = {sk, st1 + (sk - st0)};
-      [[maybe_unused]] const uint32_t sb[2] = {st0 + 2 * C::KV_BYTES + warp * kKeys * 4, st1 + 2 * C::KV_BYTES + warp * kKeys * 4};
-      // Rows hide keys behind their own position; keys from `keys` on are not of this sequence.
-      const bool border = key0 + (C::NB - 1) * kStageKeys + kKeys - 1 > pos0;
+        const uint32_t st0 = sbase + C::OFF_RING + stage * C::STAGE, st1 = sbase + C::OFF_RING + stage1 * C::STAGE;
+        const uint32_t sk = st0 + warp * (C::KV_BYTES / (D * C::ESZ / 128 > 1 ? 2 : 1) / kWarps), sv = sk + C::KV_BYTES;
+        [[maybe_unused]] const uint32_t kb[2] = {sk, st1 + (sk - st0)};
+        [[maybe_unused]] const uint32_t sb[2] = {st0 + 2 * C::KV_BYTES + warp * kKeys * 4, st1 + 2 * C::KV_BYTES + warp * kKeys * 4};
+        // Rows hide keys behind their own position; keys from `keys` on are not of this sequence.
+        const bool border = key0 + (C::NB - 1) * kStageKeys + kKeys - 1 > pos0;
 
-      if (CODE == kPlain && border) {
-        // Values that some row must not see: clear what lies behind the tile's last key, and
-        // take non-finite values out of the product (they reach the rows that see them here).
-        bool odd = false;
+        if (CODE == kPlain && border) {
+          // Values that some row must not see: clear what lies behind the tile's last key, and
+          // take non-finite values out of the product (they reach the rows that see them here).
+          bool odd = false;
 #pragma unroll
-        for (int i = 0; i < kKeys * D * 2 / 512; ++i) {
-          const int at = i * 32 + lane;            // 16-byte piece: row, piece
-          const int row = at / (D / 8), pc = at % (D / 8);
-          const uint32_t addr = sv + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
-          if (key0 + row >= keys) {
-            st_shared_v4(addr, 0u, 0u, 0u, 0u);
-          } else if (key0 + row > pos0) {
-            const uint4 x = lds128(addr);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          for (int i = 0; i < kKeys * D * 2 / 512; ++i) {
+            const int at = i * 32 + lane;            // 16-byte piece: row, piece
+            const int row = at / (D / 8), pc = at % (D / 8);
+            const uint32_t addr = sv + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
+            if (key0 + row >= keys) {
+              st_shared_v4(addr, 0u, 0u, 0u, 0u);
+            } else if (key0 + row > pos0) {
+              const uint4 x = lds128(addr);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= ((((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0);
+              for (int e = 0; e < 4; ++e) odd |= ((((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0);
+            }
           }
-        }
-        __syncwarp();
-        if (__any_sync(0xffffffffu, odd)) {
+          __syncwarp();
+          if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll 1
-          for (int row = 0; row < kKeys; ++row) {
-            if (key0 + row <= pos0 || key0 + row >= keys) continue;
+            for (int row = 0; row < kKeys; ++row) {
+              if (key0 + row <= pos0 || key0 + row >= keys) continue;
 #pragma unroll
-            for (int nt = 0; nt < C::NNT; ++nt) {  // the two columns 8 nt + 2 qj of this thread's accumulators
-              const uint32_t addr = sv + (nt >> 3) * (kStageKeys * 128) + row * 128 + (((nt & 7) ^ (row & 7)) << 4) + 4 * qj;
-              const uint32_t w = __float_as_uint(lds32(addr));
-              const float x0 = bf16_lo(w), x1 = bf16_hi(w);
-              const bool b0 = !(fabsf(x0) < INFINITY), b1 = !(fabsf(x1) < INFINITY);
+              for (int nt = 0; nt < C::NNT; ++nt) {  // the two columns 8 nt + 2 qj of this thread's accumulators
+                const uint32_t addr = sv + (nt >> 3) * (kStageKeys * 128) + row * 128 + (((nt & 7) ^ (row & 7)) << 4) + 4 * qj;
+                const uint32_t w = __float_as_uint(lds32(addr));
+                const float x0 = bf16_lo(w), x1 = bf16_hi(w);
+                const bool b0 = !(fabsf(x0) < INFINITY), b1 = !(fabsf(x1) < INFINITY);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                  if (b0 && key0 + row <= rpos[mt][hf]) o[mt][nt][2 * hf] += x0;
-                  if (b1 && key0 + row <= rpos[mt][hf]) o[mt][nt][2 * hf + 1] += x1;
-                }
-              __syncwarp();
-              if (rg == 0 && (b0 || b1))
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"((b0 ? 0u : w & 0xffffu) | (b1 ? 0u : w & 0xffff0000u)) : "memory");
+                  for (int hf = 0; hf < 2; ++hf) {
+                    if (b0 && key0 + row <= rpos[mt][hf]) o[mt][nt][2 * hf] += x0;
+                    if (b1 && key0 + row <= rpos[mt][hf]) o[mt][nt][2 * hf + 1] += x1;
+                  }
+                __syncwarp();
+                if (rg == 0 && (b0 || b1))
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"((b0 ? 0u : w & 0xffffu) | (b1 ? 0u : w & 0xffff0000u)) : "memory");
+              }
+            }
+          }
+          fence_proxy_async_smem();  // the ring's next TMA box overwrites these stores
+          __syncwarp();
+        }
+
+        // ---- S = Q K^T: two column tiles of 8 keys in each block
+        constexpr int NT = 2 * C::NB;
+        float s[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+        if constexpr (CODE == kPlain) {
+          const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+          for (int ks = 0; ks < C::NKS; ++ks) {
+            const int pc = 2 * ks + half;
+            uint32_t b[4];
+            ldsm4(b, sk + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t a[4];
+              frag(mt, ks, a);
+              mma16816(s[mt][0], a, b[0], b[1]);
+              mma16816(s[mt][1], a, b[2], b[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            uint32_t w[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int key = 8 * (n & 1) + O::key(rg);
+              uint32_t addr = kb[n >> 1];
+              if (D == 128) addr += key * 128 + (((4 * h + qj) ^ (key & 7)) << 4);
+              else addr += (key >> 1) * 128 + ((((key & 1) * 4 + qj) ^ ((key >> 1) & 7)) << 4);
+              const uint4 v = lds128(addr);
+              w[n][0] = v.x, w[n][1] = v.y, w[n][2] = v.z, w[n][3] = v.w;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t a[MT][4];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) frag(mt, 4 * h + x, a[mt]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint32_t b0 = codes_even<CODE>(w[n][x]), b1 = codes_odd<CODE>(w[n][x]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][n], a[mt], b0, b1);
+              }
             }
           }
         }
-        fence_proxy_async_smem();  // the ring's next TMA box overwrites these stores
-        __syncwarp();
-      }
 
-      // ---- S = Q K^T: two column tiles of 8 keys in each block
-      constexpr int NT = 2 * C::NB;
-      float s[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        // ---- softmax: columns 2 qj, 2 qj + 1 of each column tile
+        [[maybe_unused]] float vs[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
-      if constexpr (CODE == kPlain) {
-        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+          for (int e = 0; e < 2; ++e) {
+            const int in_block = 8 * (n & 1) + O::key(2 * qj + e), key = (n >> 1) * kStageKeys + in_block;
+            float f = P.scale_log2;
+            if constexpr (CODE != kPlain) {
+              f *= lds32(sb[n >> 1] + 4 * in_block);
+              vs[n][e] = lds32(sb[n >> 1] + kStageKeys * 4 + 4 * in_block);
+            }
 #pragma unroll
-        for (int ks = 0; ks < C::NKS; ++ks) {
-          const int pc = 2 * ks + half;
-          uint32_t b[4];
-          ldsm4(b, sk + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t a[4];
-            frag(mt, ks, a);
-            mma16816(s[mt][0], a, b[0], b[1]);
-            mma16816(s[mt][1], a, b[2], b[3]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t w[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int key = 8 * (n & 1) + O::key(rg);
-            uint32_t addr = kb[n >> 1];
-            if (D == 128) addr += key * 128 + (((4 * h + qj) ^ (key & 7)) << 4);
-            else addr += (key >> 1) * 128 + ((((key & 1) * 4 + qj) ^ ((key >> 1) & 7)) << 4);
-            const uint4 v = lds128(addr);
-            w[n][0] = v.x, w[n][1] = v.y, w[n][2] = v.z, w[n][3] = v.w;
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t a[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) frag(mt, 4 * h + x, a[mt]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t b0 = codes_even<CODE>(w[n][x]), b1 = codes_odd<CODE>(w[n][x]);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][n], a[mt], b0, b1);
+            for (int mt = 0; mt < MT; ++mt) {
+              s[mt][n][e] *= f;
+              s[mt][n][e + 2] *= f;
+              if (border) {
+                if (key0 + key > rpos[mt][0] || key0 + key >= keys) s[mt][n][e] = -INFINITY;
+                if (key0 + key > rpos[mt][1] || key0 + key >= keys) s[mt][n][e + 2] = -INFINITY;
+              }
             }
           }
-        }
-      }
-
-      // ---- softmax: columns 2 qj, 2 qj + 1 of each column tile
-      [[maybe_unused]] float vs[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int in_block = 8 * (n & 1) + O::key(2 * qj + e), key = (n >> 1) * kStageKeys + in_block;
-          float f = P.scale_log2;
-          if constexpr (CODE != kPlain) {
-            f *= lds32(sb[n >> 1] + 4 * in_block);
-            vs[n][e] = lds32(sb[n >> 1] + kStageKeys * 4 + 4 * in_block);
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            s[mt][n][e] *= f;
-            s[mt][n][e + 2] *= f;
-            if (border) {
-              if (key0 + key > rpos[mt][0] || key0 + key >= keys) s[mt][n][e] = -INFINITY;
-              if (key0 + key > rpos[mt][1] || key0 + key >= keys) s[mt][n][e + 2] = -INFINITY;
-            }
-          }
-        }
-      bool move = false;
-      float mx[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          mx[mt][hf] = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
-#pragma unroll
-          for (int n = 1; n < NT; ++n) mx[mt][hf] = fmax3(mx[mt][hf], s[mt][n][2 * hf], s[mt][n][2 * hf + 1]);
-          move |= mx[mt][hf] > m[mt][hf] + kMoveReference;
-        }
-      if (__any_sync(0xffffffffu, move)) {
+        bool move = false;
+        float mx[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float x = mx[mt][hf];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            if (x > m[mt][hf] + kMoveReference) {
-              // Before the first key o holds zeros, or infinities that the border's values have just added.
-              const float alpha = m[mt][hf] == -INFINITY ? 1.f : ex2_approx(m[mt][hf] - x);
-              m[mt][hf] = x;
-              l[mt][hf] *= alpha;
+            mx[mt][hf] = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
 #pragma unroll
-              for (int nt = 0; nt < C::NNT; ++nt) {
-                o[mt][nt][2 * hf] *= alpha;
-                o[mt][nt][2 * hf + 1] *= alpha;
+            for (int n = 1; n < NT; ++n) mx[mt][hf] = fmax3(mx[mt][hf], s[mt][n][2 * hf], s[mt][n][2 * hf + 1]);
+            move |= mx[mt][hf] > m[mt][hf] + kMoveReference;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float x = mx[mt][hf];
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              if (x > m[mt][hf] + kMoveReference) {
+                // Before the first key o holds zeros, or infinities that the border's values have just added.
+                const float alpha = m[mt][hf] == -INFINITY ? 1.f : ex2_approx(m[mt][hf] - x);
+                m[mt][hf] = x;
+                l[mt][hf] *= alpha;
+#pragma unroll
+                for (int nt = 0; nt < C::NNT; ++nt) {
+                  o[mt][nt][2 * hf] *= alpha;
+                  o[mt][nt][2 * hf + 1] *= alpha;
+                }
               }
             }
-          }
-      }
-      uint32_t pa[C::NB][MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];  // no key seen yet: 2^-inf = 0
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float p0 = ex2_approx(s[mt][n][2 * hf] - ref), p1 = ex2_approx(s[mt][n][2 * hf + 1] - ref);
-            l[mt][hf] += p0 + p1;
-            if constexpr (CODE != kPlain) {
-              p0 *= vs[n][0];
-              p1 *= vs[n][1];
-              if (border) {  // the scale of a key that is not seen may be anything
-                if (s[mt][n][2 * hf] == -INFINITY) p0 = 0.f;
-                if (s[mt][n][2 * hf + 1] == -INFINITY) p1 = 0.f;
-              }
-            }
-            pa[n >> 1][mt][2 * (n & 1) + hf] = pack_bf16x2(p0, p1);
-          }
         }
+        uint32_t pa[C::NB][MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];  // no key seen yet: 2^-inf = 0
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float p0 = ex2_approx(s[mt][n][2 * hf] - ref), p1 = ex2_approx(s[mt][n][2 * hf + 1] - ref);
+              l[mt][hf] += p0 + p1;
+              if constexpr (CODE != kPlain) {
+                p0 *= vs[n][0];
+                p1 *= vs[n][1];
+                if (border) {  // the scale of a key that is not seen may be anything
+                  if (s[mt][n][2 * hf] == -INFINITY) p0 = 0.f;
+                  if (s[mt][n][2 * hf + 1] == -INFINITY) p1 = 0.f;
+                }
+              }
+              pa[n >> 1][mt][2 * (n & 1) + hf] = pack_bf16x2(p0, p1);
+            }
+          }
 
-      // ---- O += P V
-      if constexpr (CODE == kPlain) {
-        const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
+        // ---- O += P V
+        if constexpr (CODE == kPlain) {
+          const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int pc = 2 * i + (lane >> 4);
-          uint32_t b[4];
-          ldsm4_t(b, sv + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+          for (int i = 0; i < D / 16; ++i) {
+            const int pc = 2 * i + (lane >> 4);
+            uint32_t b[4];
+            ldsm4_t(b, sv + (pc >> 3) * (kStageKeys * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(o[mt][2 * i], pa[0][mt], b[0], b[1]);
-            mma16816(o[mt][2 * i + 1], pa[0][mt], b[2], b[3]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < C::NB; ++k) {
-          const uint32_t svk = kb[k] + C::KV_BYTES;
-          uint32_t w[4][D / 32];  // the thread's four keys, D / 8 columns each
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = 8 * (x >> 1) + O::key(2 * qj + (x & 1));
-            if constexpr (D == 128) {
-              const uint4 v = lds128(svk + key * 128 + ((O::piece(rg) ^ (key & 7)) << 4));
-              w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
-            } else {
-              const uint2 v = lds64(svk + (key >> 1) * 128 + ((((key & 1) * 4 + (rg >> 1)) ^ ((key >> 1) & 7)) << 4) + (rg & 1) * 8);
-              w[x][0] = v.x, w[x][1] = v.y;
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816(o[mt][2 * i], pa[0][mt], b[0], b[1]);
+              mma16816(o[mt][2 * i + 1], pa[0][mt], b[2], b[3]);
             }
           }
+        } else {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint32_t b[4][2] = {
-                {codes_across<CODE, 0>(w[0][i], w[1][i]), codes_across<CODE, 0>(w[2][i], w[3][i])},
-                {codes_across<CODE, 1>(w[0][i], w[1][i]), codes_across<CODE, 1>(w[2][i], w[3][i])},
-                {codes_across<CODE, 2>(w[0][i], w[1][i]), codes_across<CODE, 2>(w[2][i], w[3][i])},
-                {codes_across<CODE, 3>(w[0][i], w[1][i]), codes_across<CODE, 3>(w[2][i], w[3][i])}};
+          for (int k = 0; k < C::NB; ++k) {
+            const uint32_t svk = kb[k] + C::KV_BYTES;
+            uint32_t w[4][D / 32];  // the thread's four keys, D / 8 columns each
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x) {
+              const int key = 8 * (x >> 1) + O::key(2 * qj + (x & 1));
+              if constexpr (D == 128) {
+                const uint4 v = lds128(svk + key * 128 + ((O::piece(rg) ^ (key & 7)) << 4));
+                w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+              } else {
+                const uint2 v = lds64(svk + (key >> 1) * 128 + ((((key & 1) * 4 + (rg >> 1)) ^ ((key >> 1) & 7)) << 4) + (rg & 1) * 8);
+                w[x][0] = v.x, w[x][1] = v.y;
+              }
+            }
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
+            for (int i = 0; i < D / 32; ++i) {
+              const uint32_t b[4][2] = {
+                  {codes_across<CODE, 0>(w[0][i], w[1][i]), codes_across<CODE, 0>(w[2][i], w[3][i])},
+                  {codes_across<CODE, 1>(w[0][i], w[1][i]), codes_across<CODE, 1>(w[2][i], w[3][i])},
+                  {codes_across<CODE, 2>(w[0][i], w[1][i]), codes_across<CODE, 2>(w[2][i], w[3][i])},
+                  {codes_across<CODE, 3>(w[0][i], w[1][i]), codes_across<CODE, 3>(w[2][i], w[3][i])}};
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
+            }
           }
         }
-      }
       }
       __syncwarp();  // every lane has read the stages before they are filled again
 #pragma unroll
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int CODE, int MT>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
   using C = Cfg<D, CODE, MT>;
   SmallParams P;
   P.p = p;
@@ -695,31 +709,31 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
   if (e != cudaSuccess) return e;
   paged_small<D, CODE, MT><<<kPagedCtas, kThreads, C::SMEM, st>>>(P, km, vm);
   count_launches(1);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_paged_combine(p, out, P.parts, st);
+  *parts = P.parts;
+  return cudaGetLastError();
 }
 
 // Up to 16 rows (a row tile of one mma) the second row tile would be empty.
 bool one_tile(const Paged& p) { return (long long)p.max_new * p.G <= 16; }
 
 template <int D, int CODE>
-cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
-  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, which, st) : launch<D, CODE, 2>(p, q, out, base, which, st);
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
+  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, which, st, parts) : launch<D, CODE, 2>(p, q, out, base, which, st, parts);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
-  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, which, st);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, which, st);
-  return by_rows<D, kPlain>(p, q, out, base, which, st);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
+  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, which, st, parts);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, which, st, parts);
+  return by_rows<D, kPlain>(p, q, out, base, which, st, parts);
 }
 
 }  // namespace
 
 size_t paged_small_bytes(const Paged& p) { return parts_bytes(one_tile(p) ? 16 : 32, kPagedCtas, p.D); }
 
-cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* parts_base, int which, cudaStream_t st) {
-  return p.D == 64 ? by_code<64>(p, q, out, parts_base, which, st) : by_code<128>(p, q, out, parts_base, which, st);
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, which, st, parts) : by_code<128>(p, q, out, base, which, st, parts);
 }
 
 }  // namespace tsa
