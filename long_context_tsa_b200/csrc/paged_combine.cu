@@ -22,6 +22,7 @@ constexpr int kMaxParts = 2 * kPagedCtas;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts pa, const Parts pb) {
   __shared__ float weight[kMaxParts][kRows];  // of each part: 2^(m_i - m)
+  __shared__ float total[kMaxParts][kRows];
   __shared__ float inverse[kRows];
   grid_dependency_wait();  // launched while the kernel before still runs
   const bool of_b = (int)blockIdx.x >= pa.ctas;
@@ -33,11 +34,32 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
   const int n = min(meta.c_end, parts.ctas - 1) - first + 1;
   const int rp_log2 = 7 - p.g_log2;
   auto slot = [&](int k) { return (size_t)(first + k) * 2 + (k == 0 ? 1 : 0); };
+  // Neighbouring threads take neighbouring float4s of the parts' layout.  The first parts' values are
+  // under way while the weights are found: with few parts the kernel is two round trips to L2.
+  constexpr int kItems = kRows * (D / 4) / kThreads, kFirst = 4;
+  auto row_of = [&](int j) {
+    const int i = j * kThreads + threadIdx.x;
+    return parts.by_head ? i % kRows : i / (D / 4);
+  };
+  auto col_of = [&](int j) {
+    const int i = j * kThreads + threadIdx.x;
+    return parts.by_head ? i / kRows : i % (D / 4);
+  };
+  auto source = [&](int j) {
+    return parts.o + (blockIdx.y * kRows + row_of(j)) * parts.row_stride + col_of(j) * parts.c4_stride;
+  };
+  float4 x[kItems][kFirst];
+#pragma unroll
+  for (int j = 0; j < kItems; ++j)
+#pragma unroll
+    for (int k = 0; k < kFirst; ++k)
+      if (k < n) x[j][k] = *reinterpret_cast<const float4*>(source(j) + slot(k) * parts.rows * D);
   {  // sixteen lanes for each row
     const int lr = threadIdx.x / 16, lane = threadIdx.x % 16, row = blockIdx.y * kRows + lr;
     float top = -INFINITY;
     for (int k = lane; k < n; k += 16) {
       const float m = parts.ml[slot(k) * 2 * parts.rows + row];
+      total[k][lr] = parts.ml[(slot(k) * 2 + 1) * parts.rows + row];
       weight[k][lr] = m;
       top = fmaxf(top, m);
     }
@@ -47,18 +69,16 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
     for (int k = lane; k < n; k += 16) {
       const float m = weight[k][lr], f = m == top ? 1.f : exp2f(m - top);
       weight[k][lr] = f;
-      sum += f * parts.ml[(slot(k) * 2 + 1) * parts.rows + row];
+      sum += f * total[k][lr];
     }
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) inverse[lr] = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw no key: zeros
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-    // Neighbouring threads take neighbouring float4s of the parts' layout.
-    const int lr = parts.by_head ? i % kRows : i / (D / 4);
-    const int c4 = parts.by_head ? i / kRows : i % (D / 4);
-    const int row = blockIdx.y * kRows + lr;
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const int lr = row_of(j), c4 = col_of(j), row = blockIdx.y * kRows + lr;
     int tok, head;
     if (parts.by_head) {
       tok = ((row >> 7) << rp_log2) + (row & ((1 << rp_log2) - 1));
@@ -68,17 +88,20 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
       head = row & (p.G - 1);
     }
     if (tok >= meta.n_tok) continue;
-    const float* src = parts.o + row * parts.row_stride + c4 * parts.c4_stride;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
+    auto add = [&](int k, const float4& o) {
       const float f = weight[k][lr];
-      const float4 o = *reinterpret_cast<const float4*>(src + slot(k) * parts.rows * D);
       a.x += f * o.x;
       a.y += f * o.y;
       a.z += f * o.z;
       a.w += f * o.w;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kFirst; ++k)
+      if (k < n) add(k, x[j][k]);
+    const float* src = source(j);
+#pragma unroll 8
+    for (int k = kFirst; k < n; ++k) add(k, *reinterpret_cast<const float4*>(src + slot(k) * parts.rows * D));
     const float inv = inverse[lr];
     T* dst = static_cast<T*>(out.data) + (int64_t)(meta.tok0 + tok) * out.ts + (int64_t)(meta.g * p.G + head) * out.hs + c4 * 4;
     if constexpr (sizeof(T) == 4)
