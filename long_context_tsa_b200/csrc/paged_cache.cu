@@ -76,7 +76,12 @@ __device__ __forceinline__ void pack_codes(const float (&q)[E], uint32_t (&code)
     if constexpr (CODE == kI8) {  // adding 1.5 2^23 rounds to the nearest integer, ties to even; its low byte is the code
       uint32_t m[4];
 #pragma unroll
-      for (int o = 0; o < 4; ++o) m[o] = __float_as_uint(q[e + o] + 12582912.f);
+      for (int o = 0; o < 4; o += 2) {
+        float f, g;
+        tc::f2_unpack(tc::f2_add(tc::f2_pack(q[e + o], q[e + o + 1]), tc::f2_pack(12582912.f, 12582912.f)), f, g);
+        m[o] = __float_as_uint(f);
+        m[o + 1] = __float_as_uint(g);
+      }
       code[e / 4] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
     } else {
       uint32_t h[2];
@@ -153,7 +158,11 @@ __global__ void __launch_bounds__(kThreads, 8) cache_write(const Paged p, const 
         if (E == 8 && __all_sync(0xffffffffu, a > 8.6736174e-19f && a < 1.2676506e30f)) {  // 2^-60, 2^100
           const float rinv = rcp_approx(a);
 #pragma unroll
-          for (int e = 0; e < E; ++e) q[e] = code_quotient<CODE, false>(f[e], a, rinv);
+          for (int e = 0; e < E; e += 2) {
+            q[e] = f[e];
+            q[e + 1] = f[e + 1];
+            code_quotients<CODE>(q[e], q[e + 1], a, rinv);
+          }
           scale = scale_of<CODE>(a);
         } else {
           const bool finite = top < 0x7f800000u;

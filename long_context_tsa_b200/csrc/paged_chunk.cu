@@ -132,11 +132,6 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, uint32_t x, uint32_t y) {
   float f, g;
   f2_unpack(f2_mul(f2_pack(__uint_as_float(a), __uint_as_float(b)), f2_pack(__uint_as_float(x), __uint_as_float(y))), f, g);

@@ -6,6 +6,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include "tc_ptx.cuh"
+
 namespace tsa {
 
 // Code kinds of a cache as template arguments.
@@ -22,7 +24,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// x M / a for a row whose largest magnitude is a > 0, rounded so that rounding
+// |x| M / a for a row whose largest magnitude is a > 0, rounded so that rounding
 // it once more to the code's grid gives what the exact quotient would.  r: 1 / a,
 // off by a few units in the last place at most.
 //
@@ -33,7 +35,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // fp32 holds, so every tie of a grid of at most 8 bits, comes out exact, and any
 // other within fp32's rounding.  With 8-bit significands (bf16 rows) no other
 // quotient lies within 2^-16 of a border between two codes, so this decides
-// every case.  fp32 rows (x >= 0) can come closer: next to a border b the sign of
+// every case.  fp32 rows can come closer: next to a border b the sign of
 // x M - b a decides.  Both products are known exactly there: x M as its rounded
 // value and the remainder of the rounding, and x M - b a because b has at most
 // 8 bits and the two agree in at least 12.
@@ -43,7 +45,7 @@ __device__ __forceinline__ float code_quotient(float x, float a, float r) {
   constexpr float M = code_max<CODE>();
   const float p = x * M;
   const float t0 = p * r;
-  float t = fmaf(-fmaf(t0, a, -p), r, t0);  // in this form a zero keeps its sign
+  float t = fmaf(fmaf(-t0, a, p), r, t0);
   if (WIDE) {
     float b;
     bool close;
@@ -73,6 +75,16 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+// The same for two elements at once, signs included (a zero keeps its own).
+template <int CODE>
+__device__ __forceinline__ void code_quotients(float& x, float& y, float a, float r) {
+  using namespace tc;
+  const uint64_t nr = f2_pack(-r, -r);
+  const uint64_t np = f2_mul(f2_pack(x, y), f2_pack(-code_max<CODE>(), -code_max<CODE>()));
+  const uint64_t t0 = f2_mul(np, nr);
+  f2_unpack(f2_fma(f2_fma(t0, f2_pack(a, a), np), nr, t0), x, y);
+}
+
 // Two bytes of `w` (at bits 0-7 and 16-23; the rest is ignored) as int8 -> bf16x2.
 // With the low seven bits in the mantissa of 128 .. 255, code + 128 (or + 256
 // where the sign is set) is a bf16 number, and the difference is exact.
