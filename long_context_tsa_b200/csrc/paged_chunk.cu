@@ -53,7 +53,7 @@
 #include "paged.h"
 #include "paged_codes.cuh"
 #include "paged_plan.cuh"
-#include "tc_ptx.cuh"
+#include "paged_ptx.cuh"
 #include "tma_maps.h"
 
 namespace tsa {
@@ -109,22 +109,6 @@ struct ChunkParams {
   float scale_log2;
   uint64_t wait_limit;
 };
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
 
 // Orders uses of r after an earlier wait for TMEM loads.
 __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {

@@ -6,7 +6,7 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
-#include "tc_ptx.cuh"
+#include "paged_ptx.cuh"
 
 namespace tsa {
 
