@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -399,21 +400,26 @@ def alloc_paged_workspace(desc: TsaPagedDesc, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _rows(t: torch.Tensor, desc: TsaPagedDesc, heads: int, index: int) -> TsaRows:
+_unpack_paged = struct.Struct("11if").unpack_from
+
+
+def _rows(t: torch.Tensor, shape, dtype: int, index: int) -> TsaRows:
     stride = t.stride()
-    if t.shape != (desc.n_tokens, heads, desc.D) or _DTYPES.get(t.dtype) != desc.dtype or stride[2] != 1:
-        raise ValueError(f"expected packed rows [{desc.n_tokens}, {heads}, {desc.D}] of the layer's type with unit last stride")
+    if t.shape != shape or _DTYPES.get(t.dtype) != dtype or stride[2] != 1:
+        raise ValueError(f"expected packed rows {list(shape)} of the layer's type with unit last stride")
     if t.get_device() != index:
         raise ValueError(f"tensor on {t.device}, cache on device {index}")
     return TsaRows(t.data_ptr(), stride[0], stride[1])
 
 
-def _paged_call(name: str, desc, cache, a, b, heads: int, ws, stream):
-    # A decoding step makes this call for every layer: the checks are kept to a few hundred ns each.
+def _paged_call(name: str, desc, cache, a, b, attend: bool, ws, stream):
+    # A decoding step makes this call for every layer: the checks are kept to some 100 ns each.
+    T, S, Hq, Hkv, D, dtype, cache_dtype, page_size, n_pages, max_pages, _, _ = _unpack_paged(desc)
     index = cache._index
-    if cache._shape != (desc.n_pages, desc.Hkv, desc.page_size, desc.D, desc.cache_dtype, desc.n_seqs, desc.max_pages):
+    if cache._shape != (n_pages, Hkv, page_size, D, cache_dtype, S, max_pages):
         raise ValueError(f"{name}: the cache's buffers do not have the shape that desc says")
-    ra, rb = _rows(a, desc, heads, index), _rows(b, desc, heads, index)
+    shape = (T, Hq if attend else Hkv, D)
+    ra, rb = _rows(a, shape, dtype, index), _rows(b, shape, dtype, index)
     if ws.get_device() != index or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"{name}: the workspace must be contiguous uint8 on the cache's device")
     if index < 0:
@@ -423,7 +429,7 @@ def _paged_call(name: str, desc, cache, a, b, heads: int, ws, stream):
     else:
         stream = getattr(stream, "cuda_stream", stream)
     f = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         code = f(desc, cache._c, ra, rb, ws.data_ptr(), ws.numel(), stream)
     else:
         with torch.cuda.device(index):
@@ -434,14 +440,14 @@ def _paged_call(name: str, desc, cache, a, b, heads: int, ws, stream):
 
 def tsa_cache_write(desc, cache, k, v, ws, stream=None):
     """The new tokens' keys and values [n_tokens, Hkv, D] into their pages (8-bit pools: codes and scales)."""
-    _paged_call("tsa_cache_write", desc, cache, k, v, desc.Hkv, ws, stream)
+    _paged_call("tsa_cache_write", desc, cache, k, v, False, ws, stream)
 
 
 def tsa_cache_read(desc, cache, k, v, ws, stream=None):
     """k and v [n_tokens, Hkv, D] receive the cached rows at their tokens' positions."""
-    _paged_call("tsa_cache_read", desc, cache, k, v, desc.Hkv, ws, stream)
+    _paged_call("tsa_cache_read", desc, cache, k, v, False, ws, stream)
 
 
 def tsa_attend_paged(desc, cache, q, out, ws, stream=None):
     """out [n_tokens, Hq, D]: causal attention of the new tokens q over everything cached up to their own positions."""
-    _paged_call("tsa_attend_paged", desc, cache, q, out, desc.Hq, ws, stream)
+    _paged_call("tsa_attend_paged", desc, cache, q, out, True, ws, stream)
