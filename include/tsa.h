@@ -339,7 +339,8 @@ TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t wi
  * Pools   k_pages, v_pages [n_pages][Hkv][page_size][D] in cache_dtype: the
  *         layer's dtype, TSA_I8 or TSA_E4M3.  8-bit pools have one float scale
  *         for each row of D values: k_scales, v_scales [n_pages][Hkv][page_size];
- *         a row stands for the values code * scale.  NULL scales otherwise.
+ *         a row stands for the values code * scale (an e4m3 NaN code, which
+ *         tsa_cache_write never makes, counts as +-480).  NULL scales otherwise.
  * Table   page_table int32 [n_seqs][max_pages]: position j of sequence s is slot
  *         j % page_size of page page_table[s][j / page_size].  Entries beyond
  *         the sequence's length are not read.  Pages may be shared by sequences.

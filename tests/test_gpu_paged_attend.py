@@ -144,6 +144,123 @@ def test_equal_calls_give_equal_bits_and_do_not_depend_on_max_new_or_the_workspa
     c.check(attend(c, q), q)
 
 
+@pytest.mark.parametrize("dtype,cache", CACHES)
+@pytest.mark.parametrize("news", [(40, 40), (40, 1), (12, 30)])
+def test_captured_chunks_equal_eager_ones(dtype, cache, news):
+    c = Layer([(500, news[0]), (333, news[1]), (70, 0)], Hkv=2, G=4, D=128, dtype=dtype, cache=cache, page=32, pad=1)
+    q, k, v = c.packed(8), c.packed(2), c.packed(2)
+    out = c.packed(8, random=False, fill=7.0)
+    T.tsa_cache_write(c.desc, c.cache, k, v, c.ws)
+    T.tsa_attend_paged(c.desc, c.cache, q, out, c.ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        T.tsa_cache_write(c.desc, c.cache, k, v, c.ws)
+        T.tsa_attend_paged(c.desc, c.cache, q, out, c.ws)
+    for _ in range(3):
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=c.g).to(t.dtype))
+        out.fill_(7.0)
+        graph.replay()
+        assert T.tsa_check_status(c.ws) == 0
+        c.check(out, q)
+        got = out.clone()
+        assert torch.equal(attend(c, q), got)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", None), ("bf16", "e4m3"), ("f32", None)])
+@pytest.mark.parametrize("n", [1, 60])
+def test_shared_pages_broadcast_queries_and_sizes_off_the_powers_of_two(dtype, cache, n):
+    # Three KV heads, pages of 1024; two sequences whose first pages are the same and one that repeats a page;
+    # the same query for every head and for every token.
+    c = Layer([(2500, n), (2200, n), (1100, n)], Hkv=3, G=2, D=64, dtype=dtype, cache=cache, page=1024, seed=8)
+    c.table[1, :2] = c.table[0, :2]
+    c.table[2, 1] = c.table[2, 0]
+    c.table_dev.copy_(c.table)
+    one = c.packed(1)
+    q = one.expand(c.rows, 6, 64)
+    c.check(attend(c, q), q)
+    q = one[:1].expand(c.rows, 6, 64)
+    assert q.stride(0) == 0 and q.stride(1) == 0
+    c.check(attend(c, q), q)
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+@pytest.mark.parametrize("total,n", [(700, 130), (700, 1), (129, 129), (193, 100), (65, 40)])
+def test_a_maximum_that_grows_with_every_step(dtype, cache, total, n):
+    # Each key tile's largest logit passes the one before by more than the reference tolerates, to the last step.
+    c = Layer([(total, total)], Hkv=1, G=4, D=64, dtype=dtype, cache=cache, page=32, scale=1.0, seed=7)
+    k, v = c.packed(1), c.packed(1)
+    k[..., 0] = (torch.arange(total, device=DEV) * 0.035).to(k.dtype)[:, None]
+    T.tsa_cache_write(c.desc, c.cache, k, v, c.ws)
+    c.lens, c.starts, c.rows = [(total, n)], [0, n], n
+    c.token_start.copy_(torch.tensor(c.starts))
+    c.finish()
+    q = c.packed(4) * 0.25
+    q[..., 0] = 4.0
+    c.check(attend(c, q), q)
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+def test_more_new_tokens_than_max_new_says(dtype, cache):
+    c = Layer([(300, 150), (40, 40)], Hkv=1, G=4, D=128, dtype=dtype, cache=cache, page=16)
+    c.desc.max_new = 1
+    c.ws = T.alloc_paged_workspace(c.desc)
+    q = c.packed(4)
+    c.check(attend(c, q), q)
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+def test_no_new_tokens_at_all(dtype, cache):
+    for most in (1, 100):
+        c = Layer([(5, 0), (9, 0)], Hkv=2, G=2, D=64, dtype=dtype, cache=cache, page=16, pad=2)
+        c.desc.max_new = most
+        c.ws = T.alloc_paged_workspace(c.desc)
+        c.ws[256:].fill_(0xFF)
+        assert (attend(c, c.packed(4)) == 7.0).all()
+        k = c.packed(2)
+        before = c.k_pages.clone()
+        T.tsa_cache_write(c.desc, c.cache, k, k, c.ws)
+        out = c.packed(2, random=False, fill=7.0)
+        T.tsa_cache_read(c.desc, c.cache, out, out, c.ws)
+        assert T.tsa_check_status(c.ws) == 0 and (out == 7.0).all() and torch.equal(c.k_pages.view(torch.uint8), before.view(torch.uint8))
+
+
+@pytest.mark.parametrize("cache", [None, "int8"])
+def test_chunks_on_two_streams_at_once(cache):
+    cs = [Layer([(3000 + 500 * i, 300), (700, 1)], Hkv=2, G=4, D=128, cache=cache, page=64, seed=i) for i in range(2)]
+    qs = [c.packed(8) for c in cs]
+    outs = [c.packed(8, random=False) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(20):
+        for c, q, o, st in zip(cs, qs, outs, streams):
+            T.tsa_attend_paged(c.desc, c.cache, q, o, c.ws, stream=st)
+    torch.cuda.synchronize()
+    for c, q, o in zip(cs, qs, outs):
+        assert T.tsa_check_status(c.ws) == 0
+        c.check(o, q)
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+def test_many_chunk_shapes_again_and_again(dtype, cache):
+    # Segments of one to many steps, cut at every place: barriers' phases run through all their orders.
+    g = np.random.default_rng(1)
+    for trial in range(12):
+        lens = []
+        for _ in range(int(g.integers(1, 7))):
+            n = int(g.integers(1, 1400))
+            lens.append((n, int(g.integers(1, min(n, 400) + 1))))
+        G = int(2 ** g.integers(0, 5))
+        c = Layer(lens, Hkv=int(g.integers(1, 4)), G=G, D=int(g.choice([64, 128])), dtype=dtype, cache=cache,
+                  page=int(2 ** g.integers(4, 9)), seed=trial)
+        q = c.packed(c.Hq)
+        out = attend(c, q)
+        c.check(out, q)
+        for _ in range(5):
+            assert torch.equal(attend(c, q), out)
+
+
 def test_captured_calls_follow_lengths_tables_and_new_rows():
     lens = [(100, 1), (40, 1), (260, 1)]
     c = Layer(lens, Hkv=2, G=4, D=128, cache="int8", page=16, spare=20)
