@@ -40,19 +40,18 @@ struct PartMeta {
   int32_t n_tok;  // tokens of the tile
 };
 struct Parts {
-  float* o;         // [ctas][2][rows][D], unnormalised
-  float* ml;        // [ctas][2][2][rows]: reference (log2 units), sum
-  PartMeta* meta;   // [ctas]
-  int rows;         // rows of a tile
+  float* o;          // [ctas][2][rows][D], unnormalised
+  float* ml;         // [ctas][2][2][rows]: reference (log2 units), sum
+  PartMeta* meta;    // [ctas], for paged_combine
+  uint32_t* arrived; // [ctas], for join_parts: parts of the tile begun by a CTA that are there; 0 between calls
+  int rows;          // rows of a tile
   int ctas;
-  int64_t row_stride, c4_stride;  // floats between rows / between groups of four columns
-  int by_head;      // 1: row = tile t * 128 + head * (128 / G) + token; 0: row = token * G + head
 };
 
 inline size_t parts_bytes(int rows, int ctas, int D) {
   return (size_t)ctas * 2 * rows * (D + 2) * sizeof(float) + (size_t)ctas * sizeof(PartMeta);
 }
-// Row-major parts at `base` (16-byte aligned).
+// Parts at `base` (16-byte aligned).
 inline Parts make_parts(void* base, int rows, int ctas, int D) {
   Parts p;
   p.o = static_cast<float*>(base);
@@ -60,24 +59,24 @@ inline Parts make_parts(void* base, int rows, int ctas, int D) {
   p.meta = reinterpret_cast<PartMeta*>(p.ml + (size_t)ctas * 4 * rows);
   p.rows = rows;
   p.ctas = ctas;
-  p.row_stride = D;
-  p.c4_stride = 4;
-  p.by_head = 0;
+  p.arrived = nullptr;
   return p;
 }
 
 cudaError_t launch_cache_write(const Paged& p, const Rows& k, const Rows& v, cudaStream_t st);
 cudaError_t launch_cache_read(const Paged& p, const Rows& k, const Rows& v, cudaStream_t st);
-// Attention: each launcher takes `base` of at least paged_*_bytes() (16-byte aligned) for the
-// partial tiles that it leaves, and says how they lie.
+// Attention: each launcher takes `base` of at least paged_*_bytes() (16-byte aligned) for its
+// partial tiles.  paged_simt and paged_small join them themselves (arrived: kMaxArrived words, zero
+// between calls); paged_chunk leaves them to paged_combine, in an order of its own: row =
+// M tile * 128 + query head * (128 / G) + token, columns in groups of four [D / 4][rows][4].
 // which: 0 every sequence, 1 those with at most kSplitRows rows, 2 the others.
+constexpr int kMaxArrived = 2 * kPagedCtas;
 size_t paged_simt_bytes(const Paged& p);
-cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts);
+cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st);
 size_t paged_small_bytes(const Paged& p);
-cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts);
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st);
 size_t paged_chunk_bytes(const Paged& p);
-cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts);
-// Joins the partial tiles of one or two kernels (b.ctas = 0: of a alone).
-cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& a, const Parts& b, cudaStream_t st);
+cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st);
+cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st);
 
 }  // namespace tsa

@@ -8,7 +8,8 @@
 namespace tsa {
 namespace {
 
-constexpr size_t kHeaderBytes = 256;
+constexpr size_t kHeaderBytes = 2048;  // status word, then from 256 on the arrival counts; tsa_workspace_init zeroes it
+static_assert(256 + kMaxArrived * sizeof(uint32_t) <= kHeaderBytes, "arrival counts");
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -101,28 +102,20 @@ tsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSA_OK : TSA_E
 // nearly twice as long).
 bool all_short(const Paged& p) { return (long long)p.max_new * p.G <= kSplitRows; }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 size_t workspace_bytes(const Paged& p) {
   if (p.dtype != TSA_BF16) return kHeaderBytes + paged_simt_bytes(p);
   if (all_short(p)) return kHeaderBytes + paged_small_bytes(p);
-  return kHeaderBytes + paged_chunk_bytes(p) + (p.S > 1 ? 256 + paged_small_bytes(p) : 0);
+  return kHeaderBytes + paged_chunk_bytes(p);  // larger than paged_small's
 }
 
-cudaError_t launch_attend(const Paged& p, const Rows& q, const Rows& out, char* base, cudaStream_t st) {
-  Parts a = {}, b = {};
-  cudaError_t e;
-  if (p.dtype != TSA_BF16) {
-    e = launch_paged_simt(p, q, out, base, st, &a);
-  } else if (all_short(p)) {
-    e = launch_paged_small(p, q, out, base, 0, st, &a);
-  } else if (p.S == 1) {
-    e = launch_paged_chunk(p, q, out, base, 0, st, &a);
-  } else {
-    e = launch_paged_small(p, q, out, base + align256(paged_chunk_bytes(p)), 1, st, &b);
-    if (e == cudaSuccess) e = launch_paged_chunk(p, q, out, base, 2, st, &a);
-  }
-  return e != cudaSuccess ? e : launch_paged_combine(p, out, a, b, st);
+cudaError_t launch_attend(const Paged& p, const Rows& q, const Rows& out, char* ws, cudaStream_t st) {
+  uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + 256);
+  char* base = ws + kHeaderBytes;
+  if (p.dtype != TSA_BF16) return launch_paged_simt(p, q, out, base, arrived, st);
+  if (all_short(p)) return launch_paged_small(p, q, out, base, arrived, 0, st);
+  if (p.S == 1) return launch_paged_chunk(p, q, out, base, 0, st);
+  const cudaError_t e = launch_paged_small(p, q, out, base, arrived, 1, st);  // one after the other: the parts share a place
+  return e != cudaSuccess ? e : launch_paged_chunk(p, q, out, base, 2, st);
 }
 
 // The checks that the three calls share; a and b: the packed tensors.
@@ -176,7 +169,7 @@ tsa_status tsa_attend_paged(const tsa_paged_desc* desc, const tsa_paged_cache* c
   Rows rq, ro;
   const tsa_status s = check_call(desc, cache, q, out, true, false, true, ws, ws_bytes, &p, &rq, &ro);
   if (s != TSA_OK) return s;
-  return cuda_status(launch_attend(p, rq, ro, static_cast<char*>(ws) + kHeaderBytes, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_attend(p, rq, ro, static_cast<char*>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

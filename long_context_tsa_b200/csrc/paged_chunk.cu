@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (int64_t)(s.c.g * p.G + hh) * P.out.hs;
       const size_t part = (size_t)blockIdx.x * 2 + (s.c.kt == 0 ? 1 : 0);
       const int prow = t * 128 + r;
-      float* po = P.parts.o + part * kChunkRows * D + prow * P.parts.row_stride;
+      float* po = P.parts.o + part * kChunkRows * D + prow * 4;  // lanes are rows: their float4s side by side
 #pragma unroll 1
       for (int q4 = 0; q4 < D / 32; ++q4) {
         uint32_t v[32];
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(po + (q4 * 8 + e) * P.parts.c4_stride) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            *reinterpret_cast<uint4*>(po + (q4 * 8 + e) * (4 * kChunkRows)) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       }
       if (!whole && valid) {
@@ -766,16 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int CODE>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
   using C = Cfg<D, CODE>;
   ChunkParams P;
   P.p = p;
   P.q = q;
   P.out = out;
   P.parts = make_parts(base, kChunkRows, kPagedCtas, D);
-  P.parts.row_stride = 4;  // lanes are rows: their float4s side by side
-  P.parts.c4_stride = 4 * kChunkRows;
-  P.parts.by_head = 1;
   P.plan.which = which;
   P.plan.kt_log2 = 7;
   P.plan.tt_log2 = 8 - p.g_log2;
@@ -797,23 +794,23 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
   if (e != cudaSuccess) return e;
   paged_chunk<D, CODE><<<kPagedCtas, kThreads, C::SMEM, st>>>(P, km, vm);
   count_launches(1);
-  *parts = P.parts;
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_paged_combine(p, out, P.parts, st);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
-  if (p.cache_dtype == TSA_I8) return launch<D, kI8>(p, q, out, base, which, st, parts);
-  if (p.cache_dtype == TSA_E4M3) return launch<D, kE4M3>(p, q, out, base, which, st, parts);
-  return launch<D, kPlain>(p, q, out, base, which, st, parts);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
+  if (p.cache_dtype == TSA_I8) return launch<D, kI8>(p, q, out, base, which, st);
+  if (p.cache_dtype == TSA_E4M3) return launch<D, kE4M3>(p, q, out, base, which, st);
+  return launch<D, kPlain>(p, q, out, base, which, st);
 }
 
 }  // namespace
 
 size_t paged_chunk_bytes(const Paged& p) { return parts_bytes(kChunkRows, kPagedCtas, p.D); }
 
-cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
-  return p.D == 64 ? by_code<64>(p, q, out, base, which, st, parts) : by_code<128>(p, q, out, base, which, st, parts);
+cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, which, st) : by_code<128>(p, q, out, base, which, st);
 }
 
 }  // namespace tsa

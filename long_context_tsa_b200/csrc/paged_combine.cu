@@ -1,9 +1,10 @@
-// Joins the partial tiles of the paged attention kernels.
+// Joins the partial tiles of paged_chunk.
 //
 // Part i of a tile has the reference m_i, the sum l_i and the unnormalised o_i;
 // with m = max m_i the result is sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,
-// added in the order of the CTAs that left the parts.  A few MB that the kernel
-// before has just written: read from L2, bound by latency.
+// added in the order of the CTAs that left the parts.  Up to 40 MB that the kernel
+// before has just written: read from L2, some 10 us.  (paged_small and paged_simt join
+// their few rows themselves; here 8 warps of a CTA would do 128 KB a part.)
 #include <math.h>
 
 #include "device_common.cuh"
@@ -17,37 +18,25 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRows = 8;  // rows of a block
-constexpr int kMaxParts = 2 * kPagedCtas;
+constexpr int kMaxParts = kPagedCtas;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts pa, const Parts pb) {
+template <int D>
+__global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const Rows out, const Parts parts) {
   __shared__ float weight[kMaxParts][kRows];  // of each part: 2^(m_i - m)
   __shared__ float total[kMaxParts][kRows];
   __shared__ float inverse[kRows];
   grid_dependency_wait();  // launched while the kernel before still runs
-  const bool of_b = (int)blockIdx.x >= pa.ctas;
-  const Parts& parts = of_b ? pb : pa;
-  const int first = blockIdx.x - (of_b ? pa.ctas : 0);
-  if ((int)blockIdx.y * kRows >= parts.rows) return;
-  const PartMeta meta = parts.meta[first];
+  const PartMeta meta = parts.meta[blockIdx.x];
   if (meta.c_end < 0) return;
-  const int n = min(meta.c_end, parts.ctas - 1) - first + 1;
+  const int first = blockIdx.x, n = min(meta.c_end, parts.ctas - 1) - first + 1;
   const int rp_log2 = 7 - p.g_log2;
   auto slot = [&](int k) { return (size_t)(first + k) * 2 + (k == 0 ? 1 : 0); };
   // Neighbouring threads take neighbouring float4s of the parts' layout.  The first parts' values are
   // under way while the weights are found: with few parts the kernel is two round trips to L2.
   constexpr int kItems = kRows * (D / 4) / kThreads, kFirst = 4;
-  auto row_of = [&](int j) {
-    const int i = j * kThreads + threadIdx.x;
-    return parts.by_head ? i % kRows : i / (D / 4);
-  };
-  auto col_of = [&](int j) {
-    const int i = j * kThreads + threadIdx.x;
-    return parts.by_head ? i / kRows : i % (D / 4);
-  };
-  auto source = [&](int j) {
-    return parts.o + (blockIdx.y * kRows + row_of(j)) * parts.row_stride + col_of(j) * parts.c4_stride;
-  };
+  auto row_of = [&](int j) { return (j * kThreads + (int)threadIdx.x) % kRows; };
+  auto col_of = [&](int j) { return (j * kThreads + (int)threadIdx.x) / kRows; };
+  auto source = [&](int j) { return parts.o + (blockIdx.y * kRows + row_of(j)) * 4 + col_of(j) * 4 * parts.rows; };
   float4 x[kItems][kFirst];
 #pragma unroll
   for (int j = 0; j < kItems; ++j)
@@ -79,14 +68,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     const int lr = row_of(j), c4 = col_of(j), row = blockIdx.y * kRows + lr;
-    int tok, head;
-    if (parts.by_head) {
-      tok = ((row >> 7) << rp_log2) + (row & ((1 << rp_log2) - 1));
-      head = (row & 127) >> rp_log2;
-    } else {
-      tok = row >> p.g_log2;
-      head = row & (p.G - 1);
-    }
+    const int tok = ((row >> 7) << rp_log2) + (row & ((1 << rp_log2) - 1)), head = (row & 127) >> rp_log2;
     if (tok >= meta.n_tok) continue;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](int k, const float4& o) {
@@ -103,35 +85,26 @@ __global__ void __launch_bounds__(kThreads) paged_combine(const Paged p, const R
 #pragma unroll 8
     for (int k = kFirst; k < n; ++k) add(k, *reinterpret_cast<const float4*>(src + slot(k) * parts.rows * D));
     const float inv = inverse[lr];
-    T* dst = static_cast<T*>(out.data) + (int64_t)(meta.tok0 + tok) * out.ts + (int64_t)(meta.g * p.G + head) * out.hs + c4 * 4;
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    else
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.data) + (int64_t)(meta.tok0 + tok) * out.ts + (int64_t)(meta.g * p.G + head) * out.hs + c4 * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& a, const Parts& b, cudaStream_t st) {
+cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st) {
   // A programmatic launch: the blocks are in place when the kernel that leaves the parts ends.
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int rows = b.ctas > 0 && b.rows > a.rows ? b.rows : a.rows;
-  cfg.gridDim = dim3(a.ctas + b.ctas, (rows + kRows - 1) / kRows);
+  cfg.gridDim = dim3(parts.ctas, (parts.rows + kRows - 1) / kRows);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  cudaError_t e;
-  if (p.dtype == TSA_BF16)
-    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 64>, p, out, a, b)
-                  : cudaLaunchKernelEx(&cfg, paged_combine<__nv_bfloat16, 128>, p, out, a, b);
-  else
-    e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<float, 64>, p, out, a, b)
-                  : cudaLaunchKernelEx(&cfg, paged_combine<float, 128>, p, out, a, b);
+  const cudaError_t e = p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine<64>, p, out, parts)
+                                  : cudaLaunchKernelEx(&cfg, paged_combine<128>, p, out, parts);
   count_launches(1);
   return e;
 }

@@ -15,7 +15,7 @@
 #include "internal.h"
 #include "paged.h"
 #include "paged_codes.cuh"
-#include "paged_plan.cuh"
+#include "paged_join.cuh"
 
 namespace tsa {
 namespace {
@@ -31,7 +31,8 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + (kKeys * KS > ROWS * PS ? kKeys * KS : ROWS * PS);  // P takes K's place
   static constexpr int OFF_ROWS = OFF_V + kKeys * D;
   static constexpr int OFF_PLAN = OFF_ROWS + 2 * kKeys;
-  static constexpr int SMEM = OFF_PLAN * 4 + (int)sizeof(PlanSmem);
+  static constexpr int OFF_LAST = OFF_PLAN + ((int)sizeof(PlanSmem) + 3) / 4;
+  static constexpr int SMEM = OFF_LAST * 4 + (int)sizeof(JoinSmem<ROWS>);
   static constexpr int CTAS = kPagedCtas * 2;  // two to an SM
 };
 
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
   Cursor cur;
   long long left, run;
   plan_start<kThreads>(p, P.plan, psm, &cur, &left, &run);
-  if (tid == 0) P.parts.meta[blockIdx.x].c_end = -1;
+  const long long all_left = left;
   const int tt = 1 << P.plan.tt_log2;
 
   while (left > 0) {
@@ -284,14 +285,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
         }
       }
     }
-    if (tid == 0 && cur.kt == 0 && kt1 < units) {
-      PartMeta mt;
-      mt.c_end = plan_last_cta(p, units - kt1, run);
-      mt.g = cur.g;
-      mt.tok0 = cur.span.tok0 + first_tok;
-      mt.n_tok = n_tok;
-      P.parts.meta[blockIdx.x] = mt;
-    }
+    if (!whole)
+      join_parts<float, D, ROWS, kThreads>(p, P.out, P.parts, reinterpret_cast<JoinSmem<ROWS>*>(sm + C::OFF_LAST),
+                                           tile_owners(run * blockIdx.x + (all_left - left), cur.kt, units, run), cur.g,
+                                           cur.span.tok0 + first_tok, n_rows, tid, [] { __syncthreads(); });
     left -= kt1 - cur.kt;
     if (left > 0) plan_next(p, P.plan, &cur);
   }
@@ -301,13 +298,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
 int rows_log2(const Paged& p) { return (long long)p.max_new * p.G <= 16 ? 4 : 6; }
 
 template <int CODE, int D, int ROWS>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
   using C = Cfg<D, ROWS>;
   SimtParams P;
   P.p = p;
   P.q = q;
   P.out = out;
   P.parts = make_parts(base, ROWS, C::CTAS, D);
+  P.parts.arrived = arrived;
   P.plan.tt_log2 = (ROWS == 16 ? 4 : 6) - p.g_log2;
   P.plan.kt_log2 = 6;
   P.plan.which = 0;
@@ -316,28 +314,27 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, c
   if (e != cudaSuccess) return e;
   paged_simt<CODE, D, ROWS><<<C::CTAS, kThreads, C::SMEM, st>>>(P);
   count_launches(1);
-  *parts = P.parts;
   return cudaGetLastError();
 }
 
 template <int CODE, int D>
-cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
-  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, st, parts) : launch<CODE, D, 64>(p, q, out, base, st, parts);
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
+  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, arrived, st) : launch<CODE, D, 64>(p, q, out, base, arrived, st);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
-  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, st, parts);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, st, parts);
-  return by_rows<kPlain, D>(p, q, out, base, st, parts);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
+  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, arrived, st);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, arrived, st);
+  return by_rows<kPlain, D>(p, q, out, base, arrived, st);
 }
 
 }  // namespace
 
 size_t paged_simt_bytes(const Paged& p) { return parts_bytes(1 << rows_log2(p), 2 * kPagedCtas, p.D); }
 
-cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, cudaStream_t st, Parts* parts) {
-  return p.D == 64 ? by_code<64>(p, q, out, base, st, parts) : by_code<128>(p, q, out, base, st, parts);
+cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, arrived, st) : by_code<128>(p, q, out, base, arrived, st);
 }
 
 }  // namespace tsa

@@ -50,7 +50,7 @@
 #include "internal.h"
 #include "paged.h"
 #include "paged_codes.cuh"
-#include "paged_plan.cuh"
+#include "paged_join.cuh"
 #include "paged_ptx.cuh"
 #include "tma_maps.h"
 
@@ -89,7 +89,8 @@ struct Cfg {
   static constexpr int OFF_ML = OFF_Q + (QSM ? MT * (D / 16) * 512 : 0);  // [8 warps][ROWS][m, l]
   static constexpr int OFF_BAR = OFF_ML + kWarps * ROWS * 8;
   static constexpr int OFF_PLAN = OFF_BAR + 2 * NS * 8 + 16;  // full and empty barriers, abort flag
-  static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanSmem);
+  static constexpr int OFF_LAST = OFF_PLAN + (int)sizeof(PlanSmem);
+  static constexpr int SMEM = OFF_LAST + (int)sizeof(JoinSmem<ROWS>);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   static constexpr int NKS = D / 16;  // k steps of QK
   static constexpr int NNT = D / 8;   // column tiles of O
@@ -172,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cursor cur;
   long long left, run;
   plan_start<kThreads>(p, P.plan, psm, &cur, &left, &run);
-  if (threadIdx.x == 0) P.parts.meta[blockIdx.x].c_end = -1;
   if (left == 0) return;
+  const long long all_left = left;
 
   if (warp >= kWarps) {
     // ------------------------------------------------------------ loads
@@ -648,14 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       work_sync();
     }
-    if (threadIdx.x == 0 && cur.kt == 0 && kt1 < units) {
-      PartMeta mt;
-      mt.c_end = plan_last_cta(p, units - kt1, run);
-      mt.g = cur.g;
-      mt.tok0 = cur.span.tok0 + first_tok;
-      mt.n_tok = n_tok;
-      P.parts.meta[blockIdx.x] = mt;
-    }
+    if (!whole)
+      join_parts<__nv_bfloat16, D, C::ROWS, kWork>(p, P.out, P.parts, reinterpret_cast<JoinSmem<C::ROWS>*>(smem + C::OFF_LAST),
+                                                   tile_owners(run * blockIdx.x + (all_left - left), cur.kt, units, run), cur.g,
+                                                   cur.span.tok0 + first_tok, n_rows, (int)threadIdx.x, work_sync);
     left -= did;
     if (left > 0) plan_next(p, P.plan, &cur);
   }
@@ -664,13 +661,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int CODE, int MT>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
   using C = Cfg<D, CODE, MT>;
   SmallParams P;
   P.p = p;
   P.q = q;
   P.out = out;
   P.parts = make_parts(base, C::ROWS, kPagedCtas, D);
+  P.parts.arrived = arrived;
   P.plan.which = which;
   P.plan.kt_log2 = C::KT_LOG2;
   P.plan.tt_log2 = (MT == 2 ? 5 : 4) - p.g_log2;
@@ -692,7 +690,6 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
   if (e != cudaSuccess) return e;
   paged_small<D, CODE, MT><<<kPagedCtas, kThreads, C::SMEM, st>>>(P, km, vm);
   count_launches(1);
-  *parts = P.parts;
   return cudaGetLastError();
 }
 
@@ -700,23 +697,23 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, i
 bool one_tile(const Paged& p) { return (long long)p.max_new * p.G <= 16; }
 
 template <int D, int CODE>
-cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
-  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, which, st, parts) : launch<D, CODE, 2>(p, q, out, base, which, st, parts);
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
+  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, arrived, which, st) : launch<D, CODE, 2>(p, q, out, base, arrived, which, st);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
-  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, which, st, parts);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, which, st, parts);
-  return by_rows<D, kPlain>(p, q, out, base, which, st, parts);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
+  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, arrived, which, st);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, arrived, which, st);
+  return by_rows<D, kPlain>(p, q, out, base, arrived, which, st);
 }
 
 }  // namespace
 
 size_t paged_small_bytes(const Paged& p) { return parts_bytes(one_tile(p) ? 16 : 32, kPagedCtas, p.D); }
 
-cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st, Parts* parts) {
-  return p.D == 64 ? by_code<64>(p, q, out, base, which, st, parts) : by_code<128>(p, q, out, base, which, st, parts);
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, arrived, which, st) : by_code<128>(p, q, out, base, arrived, which, st);
 }
 
 }  // namespace tsa

@@ -136,7 +136,7 @@ def test_equal_calls_give_equal_bits_and_do_not_depend_on_max_new_or_the_workspa
     c = Layer([(3000, 1), (77, 1), (1500, 6)], Hkv=2, G=4, D=128, dtype=dtype, cache=cache, page=64)
     q = c.packed(c.Hq)
     first = attend(c, q)
-    c.ws[256:].fill_(0xFF)  # only the header has to be zero
+    c.ws[2048:].fill_(0xFF)  # only what tsa_workspace_init zeroes has to be zero
     for _ in range(3):
         assert torch.equal(attend(c, q), first)
     c.desc.max_new = 400
@@ -216,7 +216,7 @@ def test_no_new_tokens_at_all(dtype, cache):
         c = Layer([(5, 0), (9, 0)], Hkv=2, G=2, D=64, dtype=dtype, cache=cache, page=16, pad=2)
         c.desc.max_new = most
         c.ws = T.alloc_paged_workspace(c.desc)
-        c.ws[256:].fill_(0xFF)
+        c.ws[2048:].fill_(0xFF)
         assert (attend(c, c.packed(4)) == 7.0).all()
         k = c.packed(2)
         before = c.k_pages.clone()
