@@ -15,9 +15,11 @@
 
 namespace tsa {
 
+constexpr int kJoinWeights = 8;  // parts whose weights are kept in shared memory
+
 template <int ROWS>
 struct JoinSmem {
-  float top[ROWS], inverse[ROWS];
+  float top[ROWS], inverse[ROWS], weight[kJoinWeights][ROWS];
   int last;
 };
 
@@ -47,18 +49,48 @@ __device__ __forceinline__ void join_parts(const Paged& p, const Rows& out, cons
   sync();
   if (!sm->last) return;
   auto slot = [&](int k) { return (size_t)(own.first + k) * 2 + (k == 0 ? 1 : 0); };
+  // Items are float4s of the tile; a thread has NB at a time.  The first parts of its first items are
+  // under way while the weights are found.
+  constexpr int NI = ROWS * (D / 4) / THREADS, NB = NI < 4 ? NI : 4, DEPTH = 2;
+  auto part = [&](int k, int j) {
+    const int i = j * THREADS + tid;
+    return __ldcg(reinterpret_cast<const float4*>(parts.o + (slot(k) * ROWS + i / (D / 4)) * D + i % (D / 4) * 4));
+  };
+  float4 x[DEPTH][NB];
+  auto load = [&](int k0, int j0) {
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        if (k0 + k < own.n) x[k][j] = part(k0 + k, j0 + j);
+  };
+  load(0, 0);
   {
     constexpr int L = THREADS / ROWS < 16 ? THREADS / ROWS : 16;  // lanes of a row
     const int row = tid / L, lane = tid % L;
     if (row < ROWS) {  // whole warps
-      float top = -INFINITY, sum = 0.f;
-      for (int k = lane; k < own.n; k += L) top = fmaxf(top, __ldcg(parts.ml + slot(k) * 2 * ROWS + row));
+      auto m_of = [&](int k) { return __ldcg(parts.ml + slot(k) * 2 * ROWS + row); };
+      auto l_of = [&](int k) { return __ldcg(parts.ml + (slot(k) * 2 + 1) * ROWS + row); };
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (lane + j * L < own.n) {
+          m[j] = m_of(lane + j * L);
+          l[j] = l_of(lane + j * L);
+        }
+      float top = fmaxf(m[0], m[1]), sum = 0.f;
+      for (int k = lane + 2 * L; k < own.n; k += L) top = fmaxf(top, m_of(k));
 #pragma unroll
       for (int d = 1; d < L; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      for (int k = lane; k < own.n; k += L) {
-        const float m = __ldcg(parts.ml + slot(k) * 2 * ROWS + row);
-        sum += (m == top ? 1.f : exp2f(m - top)) * __ldcg(parts.ml + (slot(k) * 2 + 1) * ROWS + row);
-      }
+      auto weight = [&](int k, float mk, float lk) {
+        const float f = mk == top ? 1.f : exp2f(mk - top);
+        if (k < kJoinWeights) sm->weight[k][row] = f;
+        sum += f * lk;
+      };
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (lane + j * L < own.n) weight(lane + j * L, m[j], l[j]);
+      for (int k = lane + 2 * L; k < own.n; k += L) weight(k, m_of(k), l_of(k));
 #pragma unroll
       for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == 0) {
@@ -68,25 +100,46 @@ __device__ __forceinline__ void join_parts(const Paged& p, const Rows& out, cons
     }
   }
   sync();
-  for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
-    const int row = i / (D / 4), c = i % (D / 4) * 4;
-    const float top = sm->top[row], inv = sm->inverse[row];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < own.n; ++k) {
-      const float m = __ldcg(parts.ml + slot(k) * 2 * ROWS + row);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(parts.o + (slot(k) * ROWS + row) * D + c));
-      const float f = m == top ? 1.f : exp2f(m - top);
-      a.x += f * o.x;
-      a.y += f * o.y;
-      a.z += f * o.z;
-      a.w += f * o.w;
+#pragma unroll 1
+  for (int j0 = 0; j0 < NI; j0 += NB) {
+    float4 a[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int k, const float4 (&o)[NB]) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int row = ((j0 + j) * THREADS + tid) / (D / 4);
+        float f;
+        if (k < kJoinWeights) {
+          f = sm->weight[k][row];
+        } else {
+          const float m = __ldcg(parts.ml + slot(k) * 2 * ROWS + row);
+          f = m == sm->top[row] ? 1.f : exp2f(m - sm->top[row]);
+        }
+        a[j].x += f * o[j].x;
+        a[j].y += f * o[j].y;
+        a[j].z += f * o[j].z;
+        a[j].w += f * o[j].w;
+      }
+    };
+#pragma unroll 1
+    for (int k0 = 0; k0 < own.n; k0 += DEPTH) {
+      if (j0 > 0 || k0 > 0) load(k0, j0);
+#pragma unroll
+      for (int k = 0; k < DEPTH; ++k)
+        if (k0 + k < own.n) add(k0 + k, x[k]);
     }
-    T* dst = static_cast<T*>(out.data) + (int64_t)(tok0 + (row >> p.g_log2)) * out.ts + (int64_t)(g * p.G + (row & (p.G - 1))) * out.hs + c;
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    else
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int i = (j0 + j) * THREADS + tid, row = i / (D / 4), c = i % (D / 4) * 4;
+      if (row >= n_rows) continue;
+      const float inv = sm->inverse[row];
+      T* dst = static_cast<T*>(out.data) + (int64_t)(tok0 + (row >> p.g_log2)) * out.ts + (int64_t)(g * p.G + (row & (p.G - 1))) * out.hs + c;
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(dst) = make_float4(a[j].x * inv, a[j].y * inv, a[j].z * inv, a[j].w * inv);
+      else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a[j].x * inv, a[j].y * inv), pack_bf16x2(a[j].z * inv, a[j].w * inv));
+    }
   }
 }
 
