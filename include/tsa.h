@@ -367,8 +367,8 @@ TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t wi
  * depend on it.  scale <= 0 selects 1/sqrt(D).
  *
  * `ws` is a device workspace of tsa_paged_workspace_size() bytes with the rules
- * of the calls above (zero-filled once; one stream at a time, captured graphs
- * included).  TSA_ERR_INVALID_ARG for a NULL or misaligned (16 bytes; table and
+ * of the calls above (tsa_workspace_init once before first use, or zero-filled;
+ * one stream at a time, captured graphs included).  TSA_ERR_INVALID_ARG for a NULL or misaligned (16 bytes; table and
  * lengths 4) pointer, a bad size or stride, or scales that do not go with
  * cache_dtype; TSA_ERR_UNSUPPORTED outside the shapes; TSA_ERR_WORKSPACE.
  * TSA_ERR_DEVICE_BOUNDS (status word): token_start outside the packed rows or
@@ -428,7 +428,7 @@ TSA_API tsa_status tsa_cache_read(const tsa_paged_desc* desc, const tsa_paged_ca
  * p the position of t in its sequence, k_j and v_j the cached rows of KV head
  * h / G.  Sums, maxima and accumulators are in float; the result is rounded once
  * to dtype.  bf16: probabilities (8-bit pools: times the value row's scale) are
- * rounded to bf16 for the second product; codes are exact.  Cached rows that a token does not see do not
+ * rounded to 16 bits for the second product; codes are exact.  Cached rows that a token does not see do not
  * influence its result, whatever they hold.  The work is split along the cached
  * tokens too and joined in a fixed order: equal calls give equal bits.
  */

@@ -32,8 +32,9 @@
 // key multiplies its logits, the scale of a value its probability, in fp32.  (Rows
 // rounded to bf16 with their scale in them: twice the error.)
 //
-// Measured: a prompt of 8192 tokens in bf16, 32/8 heads: 561 us, 980 TFLOP/s; 1023
-// tokens over 131071 in int8: 2.5 ms, 860 TFLOP/s.
+// Measured: a prompt of 8192 tokens in bf16, 32/8 heads: 561 us, 980 TFLOP/s, in
+// short runs and 620 in long ones (the power limit lowers the clock); 1023 tokens
+// over 131071 in int8: 2.6 ms, 830 TFLOP/s.
 //
 // Hidden keys have P = 0.  A hidden value row that is not finite would still give
 // 0 * inf, and memory behind the sequence's end may hold anything (codes are always

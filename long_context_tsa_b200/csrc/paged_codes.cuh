@@ -121,10 +121,29 @@ __device__ __forceinline__ uint32_t codes_next(uint32_t w) {
 }
 // bf16x2 of byte B of w0 and byte B of w1.
 template <int CODE, int B>
-__device__ __forceinline__ uint32_t codes_across(uint32_t w0, uint32_t w1) {
+__device__ __forceinline__ uint32_t codes_across_bf16(uint32_t w0, uint32_t w1) {
   constexpr uint32_t sel = (uint32_t)B | ((uint32_t)B << 4) | ((uint32_t)(B + 4) << 8) | ((uint32_t)(B + 4) << 12);
   const uint32_t w = __byte_perm(w0, w1, sel);
   return CODE == kI8 ? i8_pair(w) : e4m3_pair(w);
+}
+// f16x2 of byte B of w0 and byte B of w1; exact for both kinds.  int8 words have been through
+// codes_unsigned: with the offset code u = code + 128 in the mantissa of 1024 .. 2047, u + 1024 is an
+// f16 number, and the difference to 1152 exact.
+template <int CODE>
+__device__ __forceinline__ uint32_t codes_unsigned(uint32_t w) {
+  return CODE == kI8 ? w ^ 0x80808080u : w;
+}
+template <int CODE, int B>
+__device__ __forceinline__ uint32_t codes_across_f16(uint32_t w0, uint32_t w1) {
+  uint32_t r;
+  if (CODE == kI8) {
+    const uint32_t w = and_or(__byte_perm(w0, w1, (uint32_t)B | ((uint32_t)(B + 4) << 8)), 0x00ff00ffu, 0x64006400u);
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xE480E480u));
+  } else {
+    const uint32_t w = __byte_perm(w0, w1, (uint32_t)B | ((uint32_t)(B + 4) << 4));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  }
+  return r;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

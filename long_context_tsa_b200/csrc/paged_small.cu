@@ -17,33 +17,34 @@
 //   warps must not do it (four 131072-token int8 contexts: 363 us with a loading
 //   lane in each working warp, 287 with loading warps), and a copy covers as much
 //   of a page as a stage holds.
-// - 8-bit codes become bf16 without rounding (both kinds are exact in bf16); the
-//   scale of a key multiplies its logits, the scale of a value its probability,
-//   both in fp32.  Codes are read as whole 16-byte pieces of a row: the order of
+// - 8-bit codes become bf16 (K) and f16 (V) without rounding: both kinds are exact
+//   in both.  The scale of a key multiplies its logits, the scale of a value its
+//   probability, in fp32; that product becomes f16 (bf16 there: error against 64
+//   bits 0.0024 for 0.0017, half of it from the output's own rounding).  Codes are read as whole 16-byte pieces of a row: the order of
 //   the contraction index d, of the 16 keys and of the output columns is free as
 //   long as both operands agree, and is chosen so that a thread's pieces are
 //   contiguous, a quarter warp's fall into different banks, and K's codes need no
 //   byte moves.  The conversions (some 4 logic operations for 2 codes) are what
-//   bounds the 8-bit kernels: the ALU pipe is over 70 % busy.
+//   bounds the 8-bit kernels: the ALU pipe is 60 to 70 % busy.
 // - A step of one row tile takes a block of two stages at once for 8-bit caches,
-//   which gives the scheduler two independent halves (241 us against 257); with
+//   which gives the scheduler two independent halves (int8: 241 us against 257); with
 //   two row tiles the registers do not suffice for that (237 us against 217 for
 //   16 x 8 tokens in e4m3).
 // - The reference m of the softmax moves only when a logit passes it by 2^8
 //   (P <= 2^8, bf16's relative precision is the same there), found with one vote
 //   a block; the sum over a row's four threads waits until the tile ends.
 //
-// P is rounded to bf16 for the second product (relative 2^-9, the precision of
-// the output); sums, references and accumulators are fp32.
+// bf16 caches: P is rounded to bf16 for the second product (at most 2^-8 relative,
+// the precision of the output).  Sums, references and accumulators are fp32.
 //
 // A masked key has P = 0 exactly, also where its scale is not finite.  A value
 // row that is not finite and hidden from some row of the tile would still give
 // 0 * inf: where the causal border crosses the 16 keys, non-finite values of an
 // unscaled cache are added to the rows that see them and cleared in the tile.
 //
-// Measured: 61 sequences of up to 8192 tokens, bf16, one token each: 138 us, 5.6
-// TB/s (90 % of a copy's rate with the joining kernel); four of 131072 in int8:
-// 241 us, 4.6 TB/s; 16 of up to 32768 in e4m3, up to 8 tokens each: 217 us, 2.8 TB/s.
+// Measured: 61 sequences of up to 8192 tokens, bf16, one token each: 140 us, 5.7
+// TB/s (87 % of a copy's rate); four of 131072 in int8: 255 to 264 us, 4.3 TB/s; 16
+// of up to 32768 in e4m3, up to 8 tokens each: 251 us, 2.4 TB/s.
 #include <cuda.h>
 #include <math.h>
 
@@ -110,6 +111,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -307,6 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hf = 0; hf < 2; ++hf) rpos[mt][hf] = pos0 + min((mt * 16 + rg + 8 * hf) >> p.g_log2, n_tok - 1);
 
     float m[MT][2], l[MT][2], o[MT][C::NNT][4];
+    [[maybe_unused]] float v_unit = 1.f;
+    [[maybe_unused]] bool v_set = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt][0] = m[mt][1] = -INFINITY;
@@ -457,6 +471,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+        if constexpr (CODE != kPlain) {
+          // Probability times value scale becomes an f16 number: v_unit, a power of two, brings the largest
+          // scale so far to at most 2^6 (the product to at most 2^14, and all of it down to 2^-20 of a
+          // probability of one keeps f16's precision).  The accumulators are in its unit.  Blocks at the
+          // border hold scales that some rows must not notice: they take two bf16 products, whose range needs no unit.
+          if (!border) {
+            float top = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) top = fmaxf(top, fabsf(vs[n][e]) < INFINITY ? fabsf(vs[n][e]) : 0.f);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (v_set ? top * v_unit > 64.f : top > 0.f) {  // the same for the whole warp
+              const uint32_t e = max(__float_as_uint(top) >> 23, 31u) + 1;  // top < 2^(e - 127)
+              const float unit = __uint_as_float((127 + 6 + 127 - e) << 23), f = v_set ? unit / v_unit : 1.f;
+              v_unit = unit;
+              v_set = true;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < C::NNT; ++nt)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) vs[n][e] *= v_unit;
+        }
         bool move = false;
         float mx[MT][2];
 #pragma unroll
@@ -490,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         uint32_t pa[C::NB][MT][4];
+        [[maybe_unused]] uint32_t pl[C::NB][MT][4];  // 8 bits, border: P is the sum of two bf16 numbers
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -507,7 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (s[mt][n][2 * hf + 1] == -INFINITY) p1 = 0.f;
                 }
               }
-              pa[n >> 1][mt][2 * (n & 1) + hf] = pack_bf16x2(p0, p1);
+              const uint32_t hi = CODE == kPlain || border ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+              pa[n >> 1][mt][2 * (n & 1) + hf] = hi;
+              if (CODE != kPlain && border) pl[n >> 1][mt][2 * (n & 1) + hf] = pack_bf16x2(p0 - bf16_lo(hi), p1 - bf16_hi(hi));
             }
           }
 
@@ -541,17 +589,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[x][0] = v.x, w[x][1] = v.y;
               }
             }
+            if (border) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              const uint32_t b[4][2] = {
-                  {codes_across<CODE, 0>(w[0][i], w[1][i]), codes_across<CODE, 0>(w[2][i], w[3][i])},
-                  {codes_across<CODE, 1>(w[0][i], w[1][i]), codes_across<CODE, 1>(w[2][i], w[3][i])},
-                  {codes_across<CODE, 2>(w[0][i], w[1][i]), codes_across<CODE, 2>(w[2][i], w[3][i])},
-                  {codes_across<CODE, 3>(w[0][i], w[1][i]), codes_across<CODE, 3>(w[2][i], w[3][i])}};
+              for (int i = 0; i < D / 32; ++i) {
+                const uint32_t b[4][2] = {
+                    {codes_across_bf16<CODE, 0>(w[0][i], w[1][i]), codes_across_bf16<CODE, 0>(w[2][i], w[3][i])},
+                    {codes_across_bf16<CODE, 1>(w[0][i], w[1][i]), codes_across_bf16<CODE, 1>(w[2][i], w[3][i])},
+                    {codes_across_bf16<CODE, 2>(w[0][i], w[1][i]), codes_across_bf16<CODE, 2>(w[2][i], w[3][i])},
+                    {codes_across_bf16<CODE, 3>(w[0][i], w[1][i]), codes_across_bf16<CODE, 3>(w[2][i], w[3][i])}};
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
+                  for (int mt = 0; mt < MT; ++mt) {
+                    mma16816(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
+                    mma16816(o[mt][4 * i + x], pl[k][mt], b[x][0], b[x][1]);
+                  }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x][i] = codes_unsigned<CODE>(w[x][i]);
+                const uint32_t b[4][2] = {
+                    {codes_across_f16<CODE, 0>(w[0][i], w[1][i]), codes_across_f16<CODE, 0>(w[2][i], w[3][i])},
+                    {codes_across_f16<CODE, 1>(w[0][i], w[1][i]), codes_across_f16<CODE, 1>(w[2][i], w[3][i])},
+                    {codes_across_f16<CODE, 2>(w[0][i], w[1][i]), codes_across_f16<CODE, 2>(w[2][i], w[3][i])},
+                    {codes_across_f16<CODE, 3>(w[0][i], w[1][i]), codes_across_f16<CODE, 3>(w[2][i], w[3][i])}};
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) mma16816_f16(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
+              }
             }
           }
         }
@@ -590,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::ROWS + mt * 16 + rg + 8 * hf].x);
         f[hf] = m[mt][hf] == top ? 1.f : ex2_approx(m[mt][hf] - top);
+        if (CODE != kPlain) f[hf] *= 1.f / v_unit;
       }
       float* mine = join + (warp & 3) * 16 * D;
       auto at = [&](int hf, int nt, int e) -> float& {  // column groups of 8 swapped by row against bank conflicts

@@ -97,6 +97,10 @@ class Layer:
         """got against the fp64 result.  The bound, with u = 2^-8 for bf16 and 2^-24 for f32:
         u |out|    the result's rounding
         bf16:      u A for the probabilities' rounding (8-bit pools: with the value row's scale in them; codes are exact)
+                   8-bit pools of single tokens and short runs: the product of probability and scale is an f16 number
+                   whose subnormals round by at most 2^-25 of the unit.  The unit is at least 2^-6 / 2 times the
+                   largest scale so far, the sum of the probabilities at least 1 (the largest is, against its
+                   reference), so n keys are off by at most n 2^-25 2^-5 max |v| together: n 2^-30 max |v|
         (n + D + 64) 2^-23 (A + |out|) + (D + 8) 2^-23 B   fp32 sums over n keys and D products, exponentials
         (twice the unit roundoff for every operation: tensor cores truncate)."""
         bd = {}
@@ -108,6 +112,8 @@ class Layer:
         tol = u * W + (n + self.D + 64) * 2.0 ** -23 * (A + W) + (self.D + 8) * 2.0 ** -23 * B
         if bf16:
             tol = tol + u * A
+            if self.quantised:
+                tol = tol + n * 2.0 ** -30 * np.nanmax(np.abs(self.values("v")))
         sel = np.zeros(self.rows, bool)
         sel[self.starts[0]:self.starts[-1]] = True
         if rows is not None:
