@@ -36,9 +36,10 @@
  *   <= 0 is TSA_ERR_INVALID_ARG; a budget > L is clamped to L, as [P1] Step 3
  *   clamps k to the sequence length.
  * - `ws` is a device workspace of at least tsa_workspace_size() bytes, owned by
- *   the caller, zero-filled once before first use (tsa_workspace_init).  It
- *   holds a device status word; calls sharing one workspace must be ordered on
- *   one stream.
+ *   the caller, zero-filled once before first use (tsa_workspace_init, of which
+ *   the first 256 bytes matter: a device status word, and counts that are zero
+ *   between calls; the rest is scratch of the call that runs).  Calls sharing one
+ *   workspace, whichever they are, must be ordered on one stream.
  * - Argument errors are returned synchronously and nothing is launched.
  *   Device-side errors (a bounded wait that ran out, a failed bounds check)
  *   are recorded in the workspace status word and reported by
@@ -350,7 +351,8 @@ TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t wi
  *         token_start[s + 1] - 1, at its positions seq_len[s] - n to
  *         seq_len[s] - 1; n may be 0.
  *         Table and lengths are DEVICE memory, read by the kernels: a captured
- *         call follows them.
+ *         call follows them.  They must not change while a call that reads them
+ *         runs (after that the workspace has to be initialised again).
  * Rows    packed activations tsa_rows: element [token][head][d] at
  *         data + token * token_stride + head * head_stride + d, strides in
  *         elements, non-negative, multiples of 16 bytes; n_tokens rows in all,
@@ -368,7 +370,8 @@ TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t wi
  *
  * `ws` is a device workspace of tsa_paged_workspace_size() bytes with the rules
  * of the calls above (tsa_workspace_init once before first use, or zero-filled;
- * one stream at a time, captured graphs included).  TSA_ERR_INVALID_ARG for a NULL or misaligned (16 bytes; table and
+ * one stream at a time, captured graphs included), and may be one that they use
+ * too.  TSA_ERR_INVALID_ARG for a NULL or misaligned (16 bytes; table and
  * lengths 4) pointer, a bad size or stride, or scales that do not go with
  * cache_dtype; TSA_ERR_UNSUPPORTED outside the shapes; TSA_ERR_WORKSPACE.
  * TSA_ERR_DEVICE_BOUNDS (status word): token_start outside the packed rows or

@@ -43,10 +43,14 @@ struct Parts {
   float* o;          // [ctas][2][rows][D], unnormalised
   float* ml;         // [ctas][2][2][rows]: reference (log2 units), sum
   PartMeta* meta;    // [ctas], for paged_combine
-  uint32_t* arrived; // [ctas], for join_parts: parts of the tile begun by a CTA that are there; 0 between calls
+  uint32_t* header;  // the workspace's first kHeaderWords words: join_parts counts there
   int rows;          // rows of a tile
   int ctas;
 };
+
+// The header that every workspace of the library begins with: no call keeps scratch there, and it is zero
+// between calls but for the status.  Word 0: status.  Word 1: never set (tsa_debug_wait_never_set).
+constexpr int kHeaderWords = 64;
 
 inline size_t parts_bytes(int rows, int ctas, int D) {
   return (size_t)ctas * 2 * rows * (D + 2) * sizeof(float) + (size_t)ctas * sizeof(PartMeta);
@@ -59,22 +63,21 @@ inline Parts make_parts(void* base, int rows, int ctas, int D) {
   p.meta = reinterpret_cast<PartMeta*>(p.ml + (size_t)ctas * 4 * rows);
   p.rows = rows;
   p.ctas = ctas;
-  p.arrived = nullptr;
+  p.header = nullptr;
   return p;
 }
 
 cudaError_t launch_cache_write(const Paged& p, const Rows& k, const Rows& v, cudaStream_t st);
 cudaError_t launch_cache_read(const Paged& p, const Rows& k, const Rows& v, cudaStream_t st);
 // Attention: each launcher takes `base` of at least paged_*_bytes() (16-byte aligned) for its
-// partial tiles.  paged_simt and paged_small join them themselves (arrived: kMaxArrived words, zero
-// between calls); paged_chunk leaves them to paged_combine, in an order of its own: row =
+// partial tiles.  paged_simt and paged_small join them themselves (header: the workspace's, where they
+// count the parts); paged_chunk leaves them to paged_combine, in an order of its own: row =
 // M tile * 128 + query head * (128 / G) + token, columns in groups of four [D / 4][rows][4].
 // which: 0 every sequence, 1 those with at most kSplitRows rows, 2 the others.
-constexpr int kMaxArrived = 2 * kPagedCtas;
 size_t paged_simt_bytes(const Paged& p);
-cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st);
+cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, cudaStream_t st);
 size_t paged_small_bytes(const Paged& p);
-cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st);
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, int which, cudaStream_t st);
 size_t paged_chunk_bytes(const Paged& p);
 cudaError_t launch_paged_chunk(const Paged& p, const Rows& q, const Rows& out, void* base, int which, cudaStream_t st);
 cudaError_t launch_paged_combine(const Paged& p, const Rows& out, const Parts& parts, cudaStream_t st);

@@ -8,8 +8,7 @@
 namespace tsa {
 namespace {
 
-constexpr size_t kHeaderBytes = 2048;  // status word, then from 256 on the arrival counts; tsa_workspace_init zeroes it
-static_assert(256 + kMaxArrived * sizeof(uint32_t) <= kHeaderBytes, "arrival counts");
+constexpr size_t kHeaderBytes = kHeaderWords * sizeof(uint32_t);  // tsa_workspace_init zeroes it
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -109,12 +108,12 @@ size_t workspace_bytes(const Paged& p) {
 }
 
 cudaError_t launch_attend(const Paged& p, const Rows& q, const Rows& out, char* ws, cudaStream_t st) {
-  uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + 256);
+  uint32_t* header = reinterpret_cast<uint32_t*>(ws);
   char* base = ws + kHeaderBytes;
-  if (p.dtype != TSA_BF16) return launch_paged_simt(p, q, out, base, arrived, st);
-  if (all_short(p)) return launch_paged_small(p, q, out, base, arrived, 0, st);
+  if (p.dtype != TSA_BF16) return launch_paged_simt(p, q, out, base, header, st);
+  if (all_short(p)) return launch_paged_small(p, q, out, base, header, 0, st);
   if (p.S == 1) return launch_paged_chunk(p, q, out, base, 0, st);
-  const cudaError_t e = launch_paged_small(p, q, out, base, arrived, 1, st);  // one after the other: the parts share a place
+  const cudaError_t e = launch_paged_small(p, q, out, base, header, 1, st);  // one after the other: the parts share a place
   return e != cudaSuccess ? e : launch_paged_chunk(p, q, out, base, 2, st);
 }
 

@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "paged.h"
+#include "paged_arrive.cuh"
 #include "paged_codes.cuh"
 #include "paged_plan.cuh"
 
@@ -23,17 +24,6 @@ struct JoinSmem {
   int last;
 };
 
-// The CTAs with a part of the tile that the cursor is at: `upos` is the cursor's place in the list of units.
-struct Owners {
-  int first, n;
-};
-__device__ __forceinline__ Owners tile_owners(long long upos, int kt, int units, long long run) {
-  Owners o;
-  o.first = (int)((upos - kt) / run);
-  o.n = (int)((upos - kt + units - 1) / run) - o.first + 1;
-  return o;
-}
-
 // Called by all THREADS threads after the CTA's part of the tile has been written; sync() is their barrier.
 // Rows are token * G + query head.
 template <typename T, int D, int ROWS, int THREADS, typename Sync>
@@ -42,8 +32,7 @@ __device__ __forceinline__ void join_parts(const Paged& p, const Rows& out, cons
   sync();  // everyone's stores are before thread 0's fence
   if (tid == 0) {
     __threadfence();
-    sm->last = atomicAdd(parts.arrived + own.first, 1u) == (uint32_t)own.n - 1;
-    if (sm->last) parts.arrived[own.first] = 0u;  // for the next call
+    sm->last = part_arrives(parts.header, own);
     __threadfence();
   }
   sync();

@@ -298,14 +298,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt(const __grid_constant_
 int rows_log2(const Paged& p) { return (long long)p.max_new * p.G <= 16 ? 4 : 6; }
 
 template <int CODE, int D, int ROWS>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, cudaStream_t st) {
   using C = Cfg<D, ROWS>;
   SimtParams P;
   P.p = p;
   P.q = q;
   P.out = out;
   P.parts = make_parts(base, ROWS, C::CTAS, D);
-  P.parts.arrived = arrived;
+  P.parts.header = header;
   P.plan.tt_log2 = (ROWS == 16 ? 4 : 6) - p.g_log2;
   P.plan.kt_log2 = 6;
   P.plan.which = 0;
@@ -318,23 +318,23 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, u
 }
 
 template <int CODE, int D>
-cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
-  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, arrived, st) : launch<CODE, D, 64>(p, q, out, base, arrived, st);
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, cudaStream_t st) {
+  return rows_log2(p) == 4 ? launch<CODE, D, 16>(p, q, out, base, header, st) : launch<CODE, D, 64>(p, q, out, base, header, st);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
-  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, arrived, st);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, arrived, st);
-  return by_rows<kPlain, D>(p, q, out, base, arrived, st);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, cudaStream_t st) {
+  if (p.cache_dtype == TSA_I8) return by_rows<kI8, D>(p, q, out, base, header, st);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<kE4M3, D>(p, q, out, base, header, st);
+  return by_rows<kPlain, D>(p, q, out, base, header, st);
 }
 
 }  // namespace
 
 size_t paged_simt_bytes(const Paged& p) { return parts_bytes(1 << rows_log2(p), 2 * kPagedCtas, p.D); }
 
-cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, cudaStream_t st) {
-  return p.D == 64 ? by_code<64>(p, q, out, base, arrived, st) : by_code<128>(p, q, out, base, arrived, st);
+cudaError_t launch_paged_simt(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, cudaStream_t st) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, header, st) : by_code<128>(p, q, out, base, header, st);
 }
 
 }  // namespace tsa

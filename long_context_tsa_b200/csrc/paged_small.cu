@@ -730,14 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int CODE, int MT>
-cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
+cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, int which, cudaStream_t st) {
   using C = Cfg<D, CODE, MT>;
   SmallParams P;
   P.p = p;
   P.q = q;
   P.out = out;
   P.parts = make_parts(base, C::ROWS, kPagedCtas, D);
-  P.parts.arrived = arrived;
+  P.parts.header = header;
   P.plan.which = which;
   P.plan.kt_log2 = C::KT_LOG2;
   P.plan.tt_log2 = (MT == 2 ? 5 : 4) - p.g_log2;
@@ -766,23 +766,23 @@ cudaError_t launch(const Paged& p, const Rows& q, const Rows& out, void* base, u
 bool one_tile(const Paged& p) { return (long long)p.max_new * p.G <= 16; }
 
 template <int D, int CODE>
-cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
-  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, arrived, which, st) : launch<D, CODE, 2>(p, q, out, base, arrived, which, st);
+cudaError_t by_rows(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, int which, cudaStream_t st) {
+  return one_tile(p) ? launch<D, CODE, 1>(p, q, out, base, header, which, st) : launch<D, CODE, 2>(p, q, out, base, header, which, st);
 }
 
 template <int D>
-cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
-  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, arrived, which, st);
-  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, arrived, which, st);
-  return by_rows<D, kPlain>(p, q, out, base, arrived, which, st);
+cudaError_t by_code(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, int which, cudaStream_t st) {
+  if (p.cache_dtype == TSA_I8) return by_rows<D, kI8>(p, q, out, base, header, which, st);
+  if (p.cache_dtype == TSA_E4M3) return by_rows<D, kE4M3>(p, q, out, base, header, which, st);
+  return by_rows<D, kPlain>(p, q, out, base, header, which, st);
 }
 
 }  // namespace
 
 size_t paged_small_bytes(const Paged& p) { return parts_bytes(one_tile(p) ? 16 : 32, kPagedCtas, p.D); }
 
-cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* arrived, int which, cudaStream_t st) {
-  return p.D == 64 ? by_code<64>(p, q, out, base, arrived, which, st) : by_code<128>(p, q, out, base, arrived, which, st);
+cudaError_t launch_paged_small(const Paged& p, const Rows& q, const Rows& out, void* base, uint32_t* header, int which, cudaStream_t st) {
+  return p.D == 64 ? by_code<64>(p, q, out, base, header, which, st) : by_code<128>(p, q, out, base, header, which, st);
 }
 
 }  // namespace tsa

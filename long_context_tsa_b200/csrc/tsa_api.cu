@@ -179,8 +179,7 @@ size_t tsa_workspace_size(const tsa_desc* desc, int32_t window) {
 
 tsa_status tsa_workspace_init(void* ws, size_t ws_bytes, void* stream) {
   if (!aligned16(ws) || ws_bytes < kHeaderBytes) return TSA_ERR_INVALID_ARG;
-  // 2048: the header of the paged-cache calls' workspaces, which also holds counts.
-  return cuda_status(cudaMemsetAsync(ws, 0, ws_bytes < 2048 ? kHeaderBytes : 2048, static_cast<cudaStream_t>(stream)));
+  return cuda_status(cudaMemsetAsync(ws, 0, kHeaderBytes, static_cast<cudaStream_t>(stream)));
 }
 
 tsa_status tsa_score(const tsa_desc* desc, const void* q, const void* k, int32_t window, float* scores,
