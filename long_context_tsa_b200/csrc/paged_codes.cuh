@@ -128,7 +128,9 @@ __device__ __forceinline__ uint32_t codes_across_bf16(uint32_t w0, uint32_t w1) 
 }
 // f16x2 of byte B of w0 and byte B of w1; exact for both kinds.  int8 words have been through
 // codes_unsigned: with the offset code u = code + 128 in the mantissa of 1024 .. 2047, u + 1024 is an
-// f16 number, and the difference to 1152 exact.
+// f16 number, and the difference to 1152 exact.  e4m3: the fields shifted into place give the value times 2^-8
+// (bias 15 against 7), subnormals included.  The conversion instruction is shorter but makes a NaN of the codes
+// 0x7f and 0xff, which count as +-480 here as everywhere else.
 template <int CODE>
 __device__ __forceinline__ uint32_t codes_unsigned(uint32_t w) {
   return CODE == kI8 ? w ^ 0x80808080u : w;
@@ -140,8 +142,9 @@ __device__ __forceinline__ uint32_t codes_across_f16(uint32_t w0, uint32_t w1) {
     const uint32_t w = and_or(__byte_perm(w0, w1, (uint32_t)B | ((uint32_t)(B + 4) << 8)), 0x00ff00ffu, 0x64006400u);
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xE480E480u));
   } else {
-    const uint32_t w = __byte_perm(w0, w1, (uint32_t)B | ((uint32_t)(B + 4) << 4));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+    constexpr uint32_t sel = (uint32_t)B | ((uint32_t)B << 4) | ((uint32_t)(B + 4) << 8) | ((uint32_t)(B + 4) << 12);
+    const uint32_t w = __byte_perm(w0, w1, sel);
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or(w, 0x80008000u, (w << 7) & 0x3f803f80u)), "r"(0x5C005C00u));  // times 2^8
   }
   return r;
 }
