@@ -431,8 +431,10 @@ TSA_API tsa_status tsa_cache_read(const tsa_paged_desc* desc, const tsa_paged_ca
  * p the position of t in its sequence, k_j and v_j the cached rows of KV head
  * h / G.  Sums, maxima and accumulators are in float; the result is rounded once
  * to dtype.  bf16: probabilities (8-bit pools: times the value row's scale) are
- * rounded to 16 bits for the second product; codes are exact.  Cached rows that a token does not see do not
- * influence its result, whatever they hold.  The work is split along the cached
+ * rounded to 16 bits for the second product: to 8 significant ones, or over 8-bit
+ * pools for up to 32 / G new tokens to 11, where a product below 2^-21 of the row's
+ * largest is off by at most 2^-32 of that one; codes are exact.  Cached rows that a
+ * token does not see do not influence its result, whatever they hold.  The work is split along the cached
  * tokens too and joined in a fixed order: equal calls give equal bits.
  */
 TSA_API tsa_status tsa_attend_paged(const tsa_paged_desc* desc, const tsa_paged_cache* cache, const tsa_rows* q,

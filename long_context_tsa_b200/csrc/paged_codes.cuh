@@ -119,18 +119,15 @@ __device__ __forceinline__ uint32_t codes_next(uint32_t w) {
   if (CODE == kI8) return i8_pair(__byte_perm(w, 0, I == 0 ? 0x4140 : 0x4342));
   return e4m3_pair(__byte_perm(w, 0, I == 0 ? 0x1404 : 0x3424));
 }
-// bf16x2 of byte B of w0 and byte B of w1.
-template <int CODE, int B>
-__device__ __forceinline__ uint32_t codes_across_bf16(uint32_t w0, uint32_t w1) {
-  constexpr uint32_t sel = (uint32_t)B | ((uint32_t)B << 4) | ((uint32_t)(B + 4) << 8) | ((uint32_t)(B + 4) << 12);
-  const uint32_t w = __byte_perm(w0, w1, sel);
-  return CODE == kI8 ? i8_pair(w) : e4m3_pair(w);
-}
-// f16x2 of byte B of w0 and byte B of w1; exact for both kinds.  int8 words have been through
+// f16x2 of byte B of w0 and byte B of w1 in units of 2^code_f16_unit, exact for both kinds.  int8 words have been through
 // codes_unsigned: with the offset code u = code + 128 in the mantissa of 1024 .. 2047, u + 1024 is an
-// f16 number, and the difference to 1152 exact.  e4m3: the fields shifted into place give the value times 2^-8
-// (bias 15 against 7), subnormals included.  The conversion instruction is shorter but makes a NaN of the codes
+// f16 number, and the difference to 1152 exact.  e4m3: the fields shifted into place give the value in units of
+// 2^8 (bias 15 against 7), subnormals included.  The conversion instruction is shorter but makes a NaN of the codes
 // 0x7f and 0xff, which count as +-480 here as everywhere else.
+template <int CODE>
+__device__ __forceinline__ constexpr float code_f16_unit() {
+  return CODE == kI8 ? 0.f : 8.f;
+}
 template <int CODE>
 __device__ __forceinline__ uint32_t codes_unsigned(uint32_t w) {
   return CODE == kI8 ? w ^ 0x80808080u : w;
@@ -144,7 +141,7 @@ __device__ __forceinline__ uint32_t codes_across_f16(uint32_t w0, uint32_t w1) {
   } else {
     constexpr uint32_t sel = (uint32_t)B | ((uint32_t)B << 4) | ((uint32_t)(B + 4) << 8) | ((uint32_t)(B + 4) << 12);
     const uint32_t w = __byte_perm(w0, w1, sel);
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or(w, 0x80008000u, (w << 7) & 0x3f803f80u)), "r"(0x5C005C00u));  // times 2^8
+    r = and_or(w, 0x80008000u, (w << 7) & 0x3f803f80u);
   }
   return r;
 }

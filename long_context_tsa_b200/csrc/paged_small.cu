@@ -20,27 +20,33 @@
 // - 8-bit codes become bf16 (K) and f16 (V) without rounding: both kinds are exact
 //   in both.  The scale of a key multiplies its logits, the scale of a value its
 //   probability, in fp32; that product becomes f16 (bf16 there: error against 64
-//   bits 0.0024 for 0.0017, half of it from the output's own rounding).  Codes are read as whole 16-byte pieces of a row: the order of
-//   the contraction index d, of the 16 keys and of the output columns is free as
-//   long as both operands agree, and is chosen so that a thread's pieces are
-//   contiguous, a quarter warp's fall into different banks, and K's codes need no
-//   byte moves.  The conversions (some 4 logic operations for 2 codes) are what
+//   bits 0.0024 for 0.0017, half of it from the output's own rounding).  f16 has too
+//   few exponents for that, so o has a reference of its own, which follows the row's
+//   largest product as m follows its largest logit: products are at most 2^15 in the
+//   unit of o, the largest so far at least 2^7, so that those down to 2^-21 of it keep
+//   f16's 11 bits and smaller ones are off by at most 2^-32 of it.  (A unit set by the
+//   scales alone loses all others to one large scale of no probability.)
+// - Codes are read as whole 16-byte pieces of a row: the order of the contraction
+//   index d, of the 16 keys and of the output columns is free as long as both
+//   operands agree, and is chosen so that a thread's pieces are contiguous, a
+//   quarter warp's fall into different banks, and K's codes need no byte moves.  The conversions (some 4 logic operations for 2 codes) are what
 //   bounds the 8-bit kernels: the ALU pipe is 60 to 70 % busy.
 // - A step of one row tile takes a block of two stages at once for 8-bit caches,
 //   which gives the scheduler two independent halves (int8: 241 us against 257); with
 //   two row tiles the registers do not suffice for that (237 us against 217 for
 //   16 x 8 tokens in e4m3).
-// - The reference m of the softmax moves only when a logit passes it by 2^8
+// - The reference m of the softmax (and o's) moves only when a logit passes it by 2^8
 //   (P <= 2^8, bf16's relative precision is the same there), found with one vote
 //   a block; the sum over a row's four threads waits until the tile ends.
 //
 // bf16 caches: P is rounded to bf16 for the second product (at most 2^-8 relative,
 // the precision of the output).  Sums, references and accumulators are fp32.
 //
-// A masked key has P = 0 exactly, also where its scale is not finite.  A value
-// row that is not finite and hidden from some row of the tile would still give
-// 0 * inf: where the causal border crosses the 16 keys, non-finite values of an
-// unscaled cache are added to the rows that see them and cleared in the tile.
+// A masked key has P = 0 exactly, also where its scale is not finite, and its scale
+// does not move o's reference.  A value row that is not finite and hidden from some
+// row of the tile would still give 0 * inf: where the causal border crosses the 16
+// keys, non-finite values of an unscaled cache are added to the rows that see them
+// and cleared in the tile.
 //
 // Measured: 61 sequences of up to 8192 tokens, bf16, one token each: 140 us, 5.7
 // TB/s (87 % of a copy's rate); four of 131072 in int8: 255 to 264 us, 4.3 TB/s; 16
@@ -70,6 +76,11 @@ static_assert(kWork * kWorkRegs + 128 * kLoadRegs <= kThreads * 168, "registers 
 constexpr int kKeys = 16;               // keys of a block: a warp's part of a stage
 constexpr int kStageKeys = kKeys * kWarps;
 constexpr float kMoveReference = 8.f;   // log2 units
+// The reference of o (8-bit caches), in log2 units.  A product at the reference is 2^kUnit; m is at most
+// kMostAbove above the reference, so that the factor between the two fits fp32; o is multiplied by no less
+// than 2^-126: what that brings down is lost in any case, but an infinity stays one.
+constexpr float kUnit = 7.f, kMostAbove = 119.f, kLeastFactor = 1.17549435e-38f;
+static_assert(kUnit + kMoveReference < 15.99f && kUnit + kMostAbove <= 126.f, "products as f16, factors as fp32");
 constexpr uint32_t kDrainPolls = 1u << 20;
 
 template <int D, int CODE, int MT>
@@ -134,6 +145,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float lds32(uint32_t addr) {
   float v;
@@ -319,12 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hf = 0; hf < 2; ++hf) rpos[mt][hf] = pos0 + min((mt * 16 + rg + 8 * hf) >> p.g_log2, n_tok - 1);
 
     float m[MT][2], l[MT][2], o[MT][C::NNT][4];
-    [[maybe_unused]] float v_unit = 1.f;
-    [[maybe_unused]] bool v_set = false;
+    [[maybe_unused]] float ro[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt][0] = m[mt][1] = -INFINITY;
       l[mt][0] = l[mt][1] = 0.f;
+      ro[mt][0] = ro[mt][1] = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < C::NNT; ++nt)
 #pragma unroll
@@ -471,39 +487,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+        bool move = false;
+        float mx[MT][2];
+        [[maybe_unused]] float tx[MT][2];  // largest logit plus log2 of the value's scale; -inf or NaN where the key is not seen
         if constexpr (CODE != kPlain) {
-          // Probability times value scale becomes an f16 number: v_unit, a power of two, brings the largest
-          // scale so far to at most 2^6 (the product to at most 2^14, and all of it down to 2^-20 of a
-          // probability of one keeps f16's precision).  The accumulators are in its unit.  Blocks at the
-          // border hold scales that some rows must not notice: they take two bf16 products, whose range needs no unit.
-          if (!border) {
-            float top = 0.f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) top = fmaxf(top, fabsf(vs[n][e]) < INFINITY ? fabsf(vs[n][e]) : 0.f);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (v_set ? top * v_unit > 64.f : top > 0.f) {  // the same for the whole warp
-              const uint32_t e = max(__float_as_uint(top) >> 23, 31u) + 1;  // top < 2^(e - 127)
-              const float unit = __uint_as_float((127 + 6 + 127 - e) << 23), f = v_set ? unit / v_unit : 1.f;
-              v_unit = unit;
-              v_set = true;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < C::NNT; ++nt)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
-            }
-          }
+          float lv[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vs[n][e] *= v_unit;
+            for (int e = 0; e < 2; ++e) lv[n][e] = lg2_approx(fabsf(vs[n][e]));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              tx[mt][hf] = -INFINITY;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) tx[mt][hf] = fmax3(tx[mt][hf], s[mt][n][2 * hf] + lv[n][0], s[mt][n][2 * hf + 1] + lv[n][1]);
+              move |= tx[mt][hf] > ro[mt][hf] + kMoveReference;
+            }
         }
-        bool move = false;
-        float mx[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -518,44 +520,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              float x = mx[mt][hf];
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              auto of_row = [](float x) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              };
+              const float x = of_row(mx[mt][hf]);
+              float alpha = 1.f;
               if (x > m[mt][hf] + kMoveReference) {
                 // Before the first key o holds zeros, or infinities that the border's values have just added.
-                const float alpha = m[mt][hf] == -INFINITY ? 1.f : ex2_approx(m[mt][hf] - x);
+                alpha = m[mt][hf] == -INFINITY ? 1.f : ex2_approx(m[mt][hf] - x);
                 m[mt][hf] = x;
                 l[mt][hf] *= alpha;
+              }
+              if constexpr (CODE != kPlain) {
+                const float y = of_row(tx[mt][hf]);
+                float r = y > ro[mt][hf] + kMoveReference && y < INFINITY ? y : ro[mt][hf];
+                r = fmaxf(r, m[mt][hf] - kMostAbove);
+                alpha = r > ro[mt][hf] ? fmaxf(ex2_approx(ro[mt][hf] - r), kLeastFactor) : 1.f;
+                ro[mt][hf] = r;
+              }
 #pragma unroll
-                for (int nt = 0; nt < C::NNT; ++nt) {
-                  o[mt][nt][2 * hf] *= alpha;
-                  o[mt][nt][2 * hf + 1] *= alpha;
-                }
+              for (int nt = 0; nt < C::NNT; ++nt) {
+                o[mt][nt][2 * hf] *= alpha;
+                o[mt][nt][2 * hf + 1] *= alpha;
               }
             }
         }
         uint32_t pa[C::NB][MT][4];
-        [[maybe_unused]] uint32_t pl[C::NB][MT][4];  // 8 bits, border: P is the sum of two bf16 numbers
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];  // no key seen yet: 2^-inf = 0
+            [[maybe_unused]] float unit = 0.f;
+            if constexpr (CODE != kPlain) unit = ex2_approx(fminf(ref - ro[mt][hf], kMostAbove) + kUnit);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float p0 = ex2_approx(s[mt][n][2 * hf] - ref), p1 = ex2_approx(s[mt][n][2 * hf + 1] - ref);
               l[mt][hf] += p0 + p1;
               if constexpr (CODE != kPlain) {
-                p0 *= vs[n][0];
-                p1 *= vs[n][1];
+                p0 = p0 * vs[n][0] * unit;
+                p1 = p1 * vs[n][1] * unit;
                 if (border) {  // the scale of a key that is not seen may be anything
                   if (s[mt][n][2 * hf] == -INFINITY) p0 = 0.f;
                   if (s[mt][n][2 * hf + 1] == -INFINITY) p1 = 0.f;
                 }
               }
-              const uint32_t hi = CODE == kPlain || border ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-              pa[n >> 1][mt][2 * (n & 1) + hf] = hi;
-              if (CODE != kPlain && border) pl[n >> 1][mt][2 * (n & 1) + hf] = pack_bf16x2(p0 - bf16_lo(hi), p1 - bf16_hi(hi));
+              pa[n >> 1][mt][2 * (n & 1) + hf] = CODE == kPlain ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
             }
           }
 
@@ -589,37 +600,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[x][0] = v.x, w[x][1] = v.y;
               }
             }
-            if (border) {
 #pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                const uint32_t b[4][2] = {
-                    {codes_across_bf16<CODE, 0>(w[0][i], w[1][i]), codes_across_bf16<CODE, 0>(w[2][i], w[3][i])},
-                    {codes_across_bf16<CODE, 1>(w[0][i], w[1][i]), codes_across_bf16<CODE, 1>(w[2][i], w[3][i])},
-                    {codes_across_bf16<CODE, 2>(w[0][i], w[1][i]), codes_across_bf16<CODE, 2>(w[2][i], w[3][i])},
-                    {codes_across_bf16<CODE, 3>(w[0][i], w[1][i]), codes_across_bf16<CODE, 3>(w[2][i], w[3][i])}};
+            for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+              for (int x = 0; x < 4; ++x) w[x][i] = codes_unsigned<CODE>(w[x][i]);
+              const uint32_t b[4][2] = {
+                  {codes_across_f16<CODE, 0>(w[0][i], w[1][i]), codes_across_f16<CODE, 0>(w[2][i], w[3][i])},
+                  {codes_across_f16<CODE, 1>(w[0][i], w[1][i]), codes_across_f16<CODE, 1>(w[2][i], w[3][i])},
+                  {codes_across_f16<CODE, 2>(w[0][i], w[1][i]), codes_across_f16<CODE, 2>(w[2][i], w[3][i])},
+                  {codes_across_f16<CODE, 3>(w[0][i], w[1][i]), codes_across_f16<CODE, 3>(w[2][i], w[3][i])}};
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) {
-                    mma16816(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
-                    mma16816(o[mt][4 * i + x], pl[k][mt], b[x][0], b[x][1]);
-                  }
-              }
-            } else {
+              for (int x = 0; x < 4; ++x)
 #pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) w[x][i] = codes_unsigned<CODE>(w[x][i]);
-                const uint32_t b[4][2] = {
-                    {codes_across_f16<CODE, 0>(w[0][i], w[1][i]), codes_across_f16<CODE, 0>(w[2][i], w[3][i])},
-                    {codes_across_f16<CODE, 1>(w[0][i], w[1][i]), codes_across_f16<CODE, 1>(w[2][i], w[3][i])},
-                    {codes_across_f16<CODE, 2>(w[0][i], w[1][i]), codes_across_f16<CODE, 2>(w[2][i], w[3][i])},
-                    {codes_across_f16<CODE, 3>(w[0][i], w[1][i]), codes_across_f16<CODE, 3>(w[2][i], w[3][i])}};
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) mma16816_f16(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
-              }
+                for (int mt = 0; mt < MT; ++mt) mma16816_f16(o[mt][4 * i + x], pa[k][mt], b[x][0], b[x][1]);
             }
           }
         }
@@ -658,8 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::ROWS + mt * 16 + rg + 8 * hf].x);
         f[hf] = m[mt][hf] == top ? 1.f : ex2_approx(m[mt][hf] - top);
-        if (CODE != kPlain) f[hf] *= 1.f / v_unit;
+        // 8 bits: o's unit against the rows' top, as its square root: the factor itself may pass fp32's range where the product does not.
+        if (CODE != kPlain) f[hf] = ro[mt][hf] == -INFINITY ? 0.f : ex2_approx(0.5f * (ro[mt][hf] - kUnit + code_f16_unit<CODE>() - top));
       }
+      auto scaled = [&](int nt, int e) { return CODE == kPlain ? o[mt][nt][e] * f[e >> 1] : o[mt][nt][e] * f[e >> 1] * f[e >> 1]; };
       float* mine = join + (warp & 3) * 16 * D;
       auto at = [&](int hf, int nt, int e) -> float& {  // column groups of 8 swapped by row against bank conflicts
         const int r = rg + 8 * hf, d = O::col(2 * qj + e, nt);
@@ -669,14 +664,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < C::NNT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) = o[mt][nt][e] * f[e >> 1];
+          for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) = scaled(nt, e);
       }
       work_sync();
       if (warp < 4) {
 #pragma unroll
         for (int nt = 0; nt < C::NNT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) += o[mt][nt][e] * f[e >> 1];
+          for (int e = 0; e < 4; ++e) at(e >> 1, nt, e & 1) += scaled(nt, e);
       }
       work_sync();
       for (int i = threadIdx.x; i < 16 * D / 4; i += kWork) {
