@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   Cursor cur;
   long long left, run;
+  grid_dependency_launch();
   plan_start<kThreads>(p, P.plan, psm, &cur, &left, &run);  // ends with __syncthreads
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;

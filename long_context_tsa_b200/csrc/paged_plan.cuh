@@ -175,7 +175,6 @@ struct PlanSmem {
 template <int THREADS>
 __device__ __forceinline__ void plan_start(const Paged& p, const Plan& pl, PlanSmem* sm, Cursor* cur, long long* left,
                                            long long* run_out) {
-  grid_dependency_launch();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int per = (p.S + THREADS - 1) / THREADS;
   const int s0 = min(p.S, t * per), s1 = min(p.S, s0 + per);
