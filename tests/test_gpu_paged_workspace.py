@@ -57,3 +57,27 @@ def test_paged_calls_of_several_shapes_share_a_workspace(dtype):
             out = c.packed(8, random=False, fill=7.0)
             T.tsa_attend_paged(c.desc, c.cache, q, out, ws)
             assert T.tsa_check_status(ws) == 0 and torch.equal(out, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_captured_graphs_and_the_sparse_path_share_a_workspace(dtype):
+    cs = [Layer(LENS[n], Hkv=2, G=4, D=128, dtype=dtype, cache=cache, page=32, seed=i) for i, (n, cache) in enumerate([("decode", "e4m3"), ("mixed", None)])]
+    qs, outs = [c.packed(8) for c in cs], [c.packed(8, random=False) for c in cs]
+    q, k, v = sparse_layer(qs[0].dtype, 1024, 3)
+    desc = T.desc_for(q, k)
+    ws = torch.zeros(max([c.ws.numel() for c in cs] + [T.tsa_workspace_size(desc, 32)]), dtype=torch.uint8, device=DEV)
+    graphs = []
+    for c, x, o in zip(cs, qs, outs):
+        T.tsa_attend_paged(c.desc, c.cache, x, o, ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            T.tsa_attend_paged(c.desc, c.cache, x, o, ws)
+    want = [o.clone() for o in outs]
+    sparse = torch.empty_like(q)
+    for order in [(0, 1), (1, 0), (0, 0), (1, 1)]:
+        for i in order:
+            outs[i].fill_(7.0)
+            T.tsa_forward(desc, q, k, v, 32, [300, 511], sparse, ws)
+            graphs[i].replay()
+            assert T.tsa_check_status(ws) == 0 and torch.equal(outs[i], want[i])
