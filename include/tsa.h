@@ -359,14 +359,15 @@ TSA_API tsa_status tsa_layer_stable(const double* history, int32_t n, int32_t wi
  *         heads Hq (q, out) or Hkv (k, v).  [tokens][heads][D] and
  *         [heads][tokens][D] are both of this form.  Written rows must not
  *         overlap one another.  Rows that belong to no sequence (behind the last
- *         one, say, where a batch is padded) are neither read nor written.
+ *         one, say, where a batch is padded) are not written and may hold anything.
  *
  * Supported: D 64 or 128; G = Hq / Hkv in {1, 2, 4, 8, 16}; dtype TSA_F32 or
  * TSA_BF16; page_size a power of two from 16 to 1024; n_seqs, Hkv <= 1024;
  * n_tokens * Hq < 2^31; n_pages * Hkv * page_size < 2^31;
  * max_pages * page_size < 2^30.  max_new is the largest number of new tokens of
- * a sequence: it chooses the kernels and the workspace's size; results do not
- * depend on it.  scale <= 0 selects 1/sqrt(D).
+ * a sequence: it chooses the kernels and the workspace's size, and with them the
+ * result's rounding, but not what is computed (a larger number of new tokens is
+ * served too).  scale <= 0 selects 1/sqrt(D).
  *
  * `ws` is a device workspace of tsa_paged_workspace_size() bytes with the rules
  * of the calls above (tsa_workspace_init once before first use, or zero-filled;
@@ -432,9 +433,12 @@ TSA_API tsa_status tsa_cache_read(const tsa_paged_desc* desc, const tsa_paged_ca
  * h / G.  Sums, maxima and accumulators are in float; the result is rounded once
  * to dtype.  bf16: probabilities (8-bit pools: times the value row's scale) are
  * rounded to 16 bits for the second product: to 8 significant ones, or over 8-bit
- * pools for up to 32 / G new tokens to 11, where a product below 2^-21 of the row's
- * largest is off by at most 2^-32 of that one; codes are exact.  Cached rows that a
- * token does not see do not influence its result, whatever they hold.  The work is split along the cached
+ * pools in the kernel for few rows (all sequences where max_new * G <= 32, otherwise
+ * those with at most 32 / G new tokens of a batch of several) to 11, a product below
+ * 2^-21 of the row's largest being off by at most 2^-32 of that one; codes are exact.
+ * The sums are not normalised before the end: 2^8 times the sum of a row's visible
+ * |v| has to fit float.  Cached rows that a token does not see do not influence its
+ * result, whatever they hold.  The work is split along the cached
  * tokens too and joined in a fixed order: equal calls give equal bits.
  */
 TSA_API tsa_status tsa_attend_paged(const tsa_paged_desc* desc, const tsa_paged_cache* cache, const tsa_rows* q,

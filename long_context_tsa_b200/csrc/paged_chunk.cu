@@ -12,7 +12,7 @@
 //   warps 0-3, 4-7  softmax and epilogue of M tile 0 / 1 (thread = TMEM lane = row)
 //   warps 8-11      preparation: Q tiles (16-byte copies into the swizzled layout);
 //                   8-bit codes -> bf16 K/V tiles; bf16 V tiles at the causal border
-//   warps 12, 14    MMA issuers (one thread) of M tile 0 / 1: S_t = Q_t K^T, O_t += P_t V
+//   warps 12, 14    MMA issuers (a whole warp each, one elected lane) of M tile 0 / 1: S_t = Q_t K^T, O_t += P_t V
 //   warp 13         loads: one TMA box or bulk copy for each page of a tile, issued
 //                   by as many lanes
 // A step is half a key tile, 64 keys.  TMEM: for each M tile two buffers of 64 columns
@@ -33,8 +33,8 @@
 // rounded to bf16 with their scale in them: twice the error.)
 //
 // Measured: a prompt of 8192 tokens in bf16, 32/8 heads: 561 us, 980 TFLOP/s, in
-// short runs and 620 in long ones (the power limit lowers the clock); 1023 tokens
-// over 131071 in int8: 2.6 ms, 830 TFLOP/s.
+// short runs and 610 to 620 in long ones (the power limit lowers the clock); 1023
+// tokens over 131071 in int8: 2.6 ms, 830 TFLOP/s.
 //
 // Hidden keys have P = 0.  A hidden value row that is not finite would still give
 // 0 * inf, and memory behind the sequence's end may hold anything (codes are always

@@ -7,8 +7,9 @@
 // be as uneven as they like and every CTA still gets the same number of key
 // tiles, read from the device's own seq_len and token_start (a captured call
 // follows them).  A tile that a run's end cuts leaves unnormalised partial
-// results, joined by a second kernel in the order of the CTAs, so the result
-// does not depend on timing.
+// results, joined in the order of the CTAs (by a second kernel for paged_chunk,
+// by the last CTA to finish the tile for the others), so the result does not
+// depend on timing.
 #pragma once
 
 #include "device_common.cuh"

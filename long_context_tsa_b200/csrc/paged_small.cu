@@ -29,12 +29,14 @@
 // - Codes are read as whole 16-byte pieces of a row: the order of the contraction
 //   index d, of the 16 keys and of the output columns is free as long as both
 //   operands agree, and is chosen so that a thread's pieces are contiguous, a
-//   quarter warp's fall into different banks, and K's codes need no byte moves.  The conversions (some 4 logic operations for 2 codes) are what
-//   bounds the 8-bit kernels: the ALU pipe is 60 to 70 % busy.
+//   quarter warp's fall into different banks, and K's codes need no byte moves.
+//   The conversions (3 or 4 integer operations for 2 codes) are what bounds the
+//   8-bit kernels: the ALU pipe is 58 % busy with one row tile, 44 % with two, where
+//   two warps a scheduler do not cover each other's waits.
 // - A step of one row tile takes a block of two stages at once for 8-bit caches,
-//   which gives the scheduler two independent halves (int8: 241 us against 257); with
-//   two row tiles the registers do not suffice for that (237 us against 217 for
-//   16 x 8 tokens in e4m3).
+//   which gives the scheduler two independent halves (int8: 241 us against 257 when
+//   it was tried); with two row tiles the registers do not suffice for that (then
+//   237 us against 217 for 16 x 8 tokens in e4m3).
 // - The reference m of the softmax (and o's) moves only when a logit passes it by 2^8
 //   (P <= 2^8, bf16's relative precision is the same there), found with one vote
 //   a block; the sum over a row's four threads waits until the tile ends.
@@ -48,9 +50,9 @@
 // keys, non-finite values of an unscaled cache are added to the rows that see them
 // and cleared in the tile.
 //
-// Measured: 61 sequences of up to 8192 tokens, bf16, one token each: 140 us, 5.7
-// TB/s (87 % of a copy's rate); four of 131072 in int8: 255 to 264 us, 4.3 TB/s; 16
-// of up to 32768 in e4m3, up to 8 tokens each: 251 us, 2.4 TB/s.
+// Measured: 61 sequences of up to 8192 tokens, bf16, one token each: 142 us, 5.6
+// TB/s (86 % of a copy's rate); four of 131072 in int8: 260 us, 4.3 TB/s; 16 of up
+// to 32768 in e4m3, up to 8 tokens each: 248 us, 2.4 TB/s.
 #include <cuda.h>
 #include <math.h>
 
